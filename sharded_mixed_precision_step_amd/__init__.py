@@ -785,6 +785,33 @@ class DeviceStepper:
         zero_control_decide(self.ctl, 0.0, True, stream=stream)
         self.since_base += 1
 
+    def quantize_params(self, copies, matrices, stream=None) -> None:
+        """The 8-bit operands of the next forward and backward products, from
+        the fp16 parameters the last single pass left current (the previous
+        ones if it was skipped); the copy is picked on the device.  `matrices`
+        is a sequence of (offset, rows, cols, (q, s) or None, (qt, st) or
+        None): a [rows, cols] weight at param_fp16[offset:], by rows for
+        x w^T and transposed for dy w.  See zero_q8_quantize_ctl."""
+        params = [cp[3] for cp in copies]
+        for offset, rows, cols, by_rows, transposed in matrices:
+            end = offset + rows * cols
+            for k, p in enumerate(params):
+                if offset < 0 or end > p.numel():
+                    raise ValueError(f"matrix [{offset}, {end}) lies outside the {p.numel()} "
+                                     f"params of copy {k}")
+            q, s = (None, None) if by_rows is None else by_rows
+            qt, st = (None, None) if transposed is None else transposed
+            zero_q8_quantize_ctl([p[offset:end].view(rows, cols) for p in params], self.ctl,
+                                 q=q, s=s, qt=qt, st=st, stream=stream)
+
+    def distill(self, logits, index, teacher, loss, lse, grad, *, temperature: float = 1.0,
+                row_weight: Optional[torch.Tensor] = None, stream=None) -> None:
+        """zero_distill with the loss scale of the next step, read on the
+        device: the gradient that this stepper's next step unscales.  To be
+        enqueued after the last step's decision and before the next one's."""
+        zero_distill(logits, index, teacher, loss, lse, grad, temperature=temperature,
+                     row_weight=row_weight, ctl=self.ctl, stream=stream)
+
     def prepare_single_pass(self, grad_chunks, copies, stream=None) -> "PreparedSinglePass":
         """single_pass with its arguments marshalled once: for short steps,
         where the per-call argument checks and pointer tables cost host time
@@ -949,3 +976,11 @@ def load_shard_state(path: str, device) -> dict:
     """The tensors save_shard_state wrote, on `device`, bit for bit."""
     from safetensors.torch import load_file
     return {k: v.to(device) for k, v in load_file(path).items()}
+
+
+# The training operators (zero_train.h): their binding needs the names above.
+from .train import (  # noqa: E402,F401
+    ZERO_BF16, ZERO_DISTILL_MAX_TOP, ZERO_E4M3, ZERO_E5M2, ZERO_F16, ZERO_F32,
+    ZERO_NORM_MAX_COLS, ZERO_NORM_MAX_PARTS, ZERO_Q8_BLOCK, ZERO_Q8_MAX_LD, q8_empty, q8_shape,
+    zero_distill, zero_distill_backward, zero_distill_forward, zero_q8_gemm, zero_q8_quantize,
+    zero_q8_quantize_ctl, zero_rmsnorm, zero_rmsnorm_backward, zero_rmsnorm_backward_workspace)

@@ -16,7 +16,11 @@ ROOT = os.path.dirname(HERE)
 INCLUDE = os.path.join(ROOT, "include")
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libzerostep.so")
-SOURCES = [os.path.join(CSRC, "zero_kernels.hip"), os.path.join(CSRC, "zero_abi.cpp")]
+SOURCES = [os.path.join(CSRC, name) for name in (
+    "zero_kernels.hip", "zero_abi.cpp",
+    # the training operators (zero_train.h)
+    "zero_train_abi.cpp", "zero_norm.hip", "zero_norm_backward.hip", "zero_q8.hip",
+    "zero_q8_gemm.hip", "zero_distill.hip")]
 TWIN_LIB = os.path.join(HERE, "libzerotwin.so")
 TWIN_SOURCES = [os.path.join(CSRC, "zero_twin.hip")]
 # the device side of the seeded input generators (workloads/), test and
@@ -89,38 +93,62 @@ def kernel_digest() -> str:
     return h.hexdigest()
 
 
-def build(verbose: bool = False) -> str:
-    """Compile the three libraries for gfx950 (hipcc processes side by side),
-    each written atomically."""
-    jobs = []
-    for lib, sources in ((LIB, SOURCES), (TWIN_LIB, TWIN_SOURCES), (GEN_LIB, GEN_SOURCES)):
-        name = os.path.basename(lib)
-        fd, tmp = tempfile.mkstemp(prefix=f".{name}.", suffix=".tmp", dir=os.path.dirname(lib))
-        os.close(fd)
-        cmd = [hipcc(), *FLAGS, "-I", INCLUDE, "-I", CSRC, "-I", GEN_DIR, *sources, "-o", tmp]
-        if verbose:
-            print(" ".join(cmd), flush=True)
-        proc = subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.PIPE, text=True)
-        jobs.append((lib, tmp, proc))
-    errors = []
+def _run_all(commands, verbose: bool) -> None:
+    """Run the commands side by side; raise with the output of those that fail."""
+    procs = []
     try:
-        for lib, tmp, proc in jobs:
+        for cmd in commands:
+            if verbose:
+                print(" ".join(cmd), flush=True)
+            procs.append((cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE,
+                                                stderr=subprocess.PIPE, text=True)))
+        errors = []
+        for cmd, proc in procs:
             out, err = proc.communicate()
             if proc.returncode != 0:
-                errors.append(f"hipcc failed ({proc.returncode}) for {os.path.basename(lib)}:"
-                              f"\n{out}\n{err}")
-                continue
-            if verbose and err.strip():
+                errors.append(f"hipcc failed ({proc.returncode}) for {cmd[-1]}:\n{out}\n{err}")
+            elif verbose and err.strip():
                 print(err, flush=True)
-            os.replace(tmp, lib)
+        if errors:
+            raise RuntimeError("\n".join(errors))
     finally:
-        for _, tmp, proc in jobs:
+        for _, proc in procs:
             if proc.poll() is None:
                 proc.kill()
-            if os.path.exists(tmp):
-                os.unlink(tmp)
-    if errors:
-        raise RuntimeError("\n".join(errors))
+
+
+def build(verbose: bool = False) -> str:
+    """Compile the three libraries for gfx950: each source to an object (hipcc
+    processes side by side), then each library from its objects, written
+    atomically."""
+    libs = ((LIB, SOURCES), (TWIN_LIB, TWIN_SOURCES), (GEN_LIB, GEN_SOURCES))
+    compile_flags = [f for f in FLAGS if f != "-shared"]
+    link_flags = [f"--offload-arch={ARCH}", "-fPIC", "-shared"]
+    temps = []
+    with tempfile.TemporaryDirectory(prefix="zerostep_build_") as objdir:
+        try:
+            compiles, links = [], []
+            for lib, sources in libs:
+                objects = []
+                for src in sources:
+                    obj = os.path.join(objdir, f"{len(compiles)}.o")
+                    objects.append(obj)
+                    compiles.append([hipcc(), *compile_flags, "-I", INCLUDE, "-I", CSRC, "-I",
+                                     GEN_DIR, "-o", obj, "-c", src])
+                name = os.path.basename(lib)
+                fd, tmp = tempfile.mkstemp(prefix=f".{name}.", suffix=".tmp",
+                                           dir=os.path.dirname(lib))
+                os.close(fd)
+                temps.append(tmp)
+                links.append((lib, tmp, [hipcc(), *link_flags, *objects, "-o", tmp]))
+            _run_all(compiles, verbose)
+            _run_all([cmd for _, _, cmd in links], verbose)
+            for lib, tmp, _ in links:
+                os.replace(tmp, lib)
+        finally:
+            for tmp in temps:
+                if os.path.exists(tmp):
+                    os.unlink(tmp)
     return LIB
 
 

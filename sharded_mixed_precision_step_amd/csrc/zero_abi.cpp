@@ -9,14 +9,13 @@
 #include <algorithm>
 #include <vector>
 
+#include "zero_host.h"
 #include "zero_internal.h"
 #include "zero_step.h"
 
-namespace {
+namespace zero {
 
-float bias_correction(float beta, int64_t t);
-
-thread_local char g_error[512] = "";
+static thread_local char g_error[512] = "";
 
 int fail(int code, const char* fmt, ...) {
     va_list ap;
@@ -36,16 +35,18 @@ int hip_fail(hipError_t e, const char* where) {
                 hipGetErrorString(e));
 }
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+}  // namespace zero
 
-bool finite_f(float x) { return isfinite(x) != 0; }
+namespace {
 
-// [a, a + na) and [b, b + nb) share a byte.
-bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return na > 0 && nb > 0 && x < y + static_cast<uintptr_t>(nb) &&
-           y < x + static_cast<uintptr_t>(na);
-}
+using zero::aligned;
+using zero::fail;
+using zero::finite_f;
+using zero::hip_fail;
+using zero::ok;
+using zero::overlap;
+
+float bias_correction(float beta, int64_t t);
 
 bool is_pow2(float x) {
     int e = 0;
@@ -481,7 +482,7 @@ struct FlattenBatcher {
 
 extern "C" {
 
-const char* zero_last_error_string(void) { return g_error; }
+const char* zero_last_error_string(void) { return zero::g_error; }
 
 int zero_overflow_check(const void* const* grad_chunks, int32_t n_chunks, int64_t n,
                         float loss_scale, int32_t* d_overflow, double* d_sqnorm, void* stream) {

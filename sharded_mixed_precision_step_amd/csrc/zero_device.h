@@ -1,0 +1,236 @@
+// Device helpers of the training operators: element types, rows of any
+// alignment, 8-bit blocks, reductions.  gfx950 only.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "zero_train.h"
+
+namespace zero {
+namespace dev {
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+// The same with an element's alignment: gfx950 loads and stores 16 bytes at
+// any address, so rows need not be 16-byte aligned.
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+typedef u32x2 u32x2_any __attribute__((aligned(2)));
+
+// By value: clang's bit cast of a vector's element takes the vector's first.
+__device__ __forceinline__ float as_float(uint32_t bits) { return __builtin_bit_cast(float, bits); }
+__device__ __forceinline__ uint32_t as_bits(float v) { return __builtin_bit_cast(uint32_t, v); }
+
+__device__ __forceinline__ float from16(uint32_t bits, bool bf16) {
+    return bf16 ? as_float(bits << 16)
+                : static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(bits)));
+}
+
+// One rounding to nearest even; beyond the range of fp16: inf.
+__device__ __forceinline__ uint32_t to16(float v, bool bf16) {
+    return bf16 ? static_cast<uint32_t>(
+                      __builtin_bit_cast(uint16_t, static_cast<__bf16>(v)))
+                : static_cast<uint32_t>(
+                      __builtin_bit_cast(uint16_t, static_cast<_Float16>(v)));
+}
+
+__device__ __forceinline__ float load1(const void* p, int64_t i, int dtype) {
+    if (dtype == ZERO_F32) return static_cast<const float*>(p)[i];
+    return from16(static_cast<const uint16_t*>(p)[i], dtype == ZERO_BF16);
+}
+
+__device__ __forceinline__ void store1(void* p, int64_t i, int dtype, float v) {
+    if (dtype == ZERO_F32)
+        static_cast<float*>(p)[i] = v;
+    else
+        static_cast<uint16_t*>(p)[i] = static_cast<uint16_t>(to16(v, dtype == ZERO_BF16));
+}
+
+// Eight consecutive elements as loaded: 16 bytes of a 16-bit type, 32 of fp32.
+template <int BYTES>
+struct Raw8 {
+    u32x4 v[BYTES == 4 ? 2 : 1];
+};
+
+// Elements i .. i + 7 of p, of which the first n (may be <= 0) exist; the
+// others read as zero.
+template <int BYTES>
+__device__ __forceinline__ Raw8<BYTES> load8(const void* p, int64_t i, int n) {
+    Raw8<BYTES> r;
+    const char* at = static_cast<const char*>(p) + i * BYTES;
+    if (n >= 8) {
+#pragma unroll
+        for (int k = 0; k < BYTES / 2; ++k)
+            r.v[k] = reinterpret_cast<const u32x4_any*>(at)[k];
+        return r;
+    }
+#pragma unroll
+    for (int k = 0; k < BYTES / 2; ++k) r.v[k] = u32x4{0, 0, 0, 0};
+    if (n > 0) {
+        if constexpr (BYTES == 4) {
+            const uint32_t* q = reinterpret_cast<const uint32_t*>(at);
+#pragma unroll
+            for (int k = 0; k < 7; ++k)
+                if (k < n) r.v[k / 4][k % 4] = q[k];
+        } else {
+            const uint16_t* q = reinterpret_cast<const uint16_t*>(at);
+#pragma unroll
+            for (int k = 0; k < 7; ++k)
+                if (k < n) r.v[0][k / 2] |= static_cast<uint32_t>(q[k]) << (16 * (k % 2));
+        }
+    }
+    return r;
+}
+
+template <int BYTES>
+__device__ __forceinline__ void widen8(const Raw8<BYTES>& r, bool bf16, float (&f)[8]) {
+    if constexpr (BYTES == 4) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) f[k] = as_float(r.v[k / 4][k % 4]);
+    } else {
+        if (bf16) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                f[k] = as_float(k % 2 ? r.v[0][k / 2] & 0xffff0000u : r.v[0][k / 2] << 16);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) f[k] = from16(r.v[0][k / 2] >> (16 * (k % 2)), false);
+        }
+    }
+}
+
+// Stores the first n (at most 8) of f as elements i .. of p.
+template <bool NT = false>
+__device__ __forceinline__ void store8(void* p, int64_t i, int n, int dtype, const float (&f)[8]) {
+    if (n <= 0) return;
+    if (n >= 8) {
+        if (dtype == ZERO_F32) {
+            u32x4_any* at = reinterpret_cast<u32x4_any*>(static_cast<float*>(p) + i);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                u32x4 v;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[j] = as_bits(f[4 * k + j]);
+                if constexpr (NT) __builtin_nontemporal_store(v, at + k);
+                else at[k] = v;
+            }
+        } else {
+            u32x4 v;
+            if (dtype == ZERO_BF16) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    v[k] = to16(f[2 * k], true) | to16(f[2 * k + 1], true) << 16;
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    v[k] = to16(f[2 * k], false) | to16(f[2 * k + 1], false) << 16;
+            }
+            u32x4_any* at = reinterpret_cast<u32x4_any*>(static_cast<uint16_t*>(p) + i);
+            if constexpr (NT) __builtin_nontemporal_store(v, at);
+            else *at = v;
+        }
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < 7; ++k)
+        if (k < n) store1(p, i + k, dtype, f[k]);
+}
+
+// ---- 8-bit blocks --------------------------------------------------------
+
+struct BlockScale {
+    float inv;     // 2^-e
+    uint32_t byte; // e + 127, or 255
+};
+
+// The scale of a block whose largest magnitude has these fp32 bits (sign
+// cleared).  Both 8-bit types' largest value is 1.75 * 2^top (448 = 1.75 * 2^8,
+// 57344 = 1.75 * 2^15), so the smallest e with amax <= 1.75 * 2^(top + e) is
+// amax's own exponent less top, one more if its mantissa is above 1.75.  A
+// NaN's or inf's bits compare above every finite value's.
+__device__ __forceinline__ BlockScale block_scale(uint32_t amax_bits, int fmt) {
+    const int top = fmt == ZERO_E4M3 ? 8 : 15;
+    int e = static_cast<int>(amax_bits >> 23) - 127 - top + ((amax_bits & 0x7fffffu) > 0x600000u);
+    e = e < -127 ? -127 : e;
+    if (amax_bits == 0) e = 0;
+    BlockScale r;
+    r.inv = as_float(static_cast<uint32_t>(127 - e) << 23);
+    r.byte = amax_bits >= 0x7f800000u ? 255u : static_cast<uint32_t>(e + 127);
+    return r;
+}
+
+// Four scaled values as 8-bit floats, rounded to nearest even.
+__device__ __forceinline__ uint32_t pack4(float a, float b, float c, float d, int fmt) {
+    int r;
+    if (fmt == ZERO_E4M3) {
+        r = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+        r = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, r, true);
+    } else {
+        r = __builtin_amdgcn_cvt_pk_bf8_f32(a, b, 0, false);
+        r = __builtin_amdgcn_cvt_pk_bf8_f32(c, d, r, true);
+    }
+    return static_cast<uint32_t>(r);
+}
+
+__device__ __forceinline__ u32x2 pack8(const float (&f)[8], const BlockScale& s, int fmt) {
+    if (s.byte == 255u) return u32x2{0x7f7f7f7fu, 0x7f7f7f7fu};  // NaN in both types
+    u32x2 r;
+    r[0] = pack4(f[0] * s.inv, f[1] * s.inv, f[2] * s.inv, f[3] * s.inv, fmt);
+    r[1] = pack4(f[4] * s.inv, f[5] * s.inv, f[6] * s.inv, f[7] * s.inv, fmt);
+    return r;
+}
+
+__device__ __forceinline__ uint32_t abs_bits(float v) {
+    return as_bits(v) & 0x7fffffffu;
+}
+
+__device__ __forceinline__ uint32_t amax8(const float (&f)[8]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const uint32_t b = abs_bits(f[k]);
+        m = b > m ? b : m;
+    }
+    return m;
+}
+
+__device__ __forceinline__ uint32_t max16lanes(uint32_t m) {
+#pragma unroll
+    for (int d = 1; d < 16; d *= 2) {
+        const uint32_t o = static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), d));
+        m = o > m ? o : m;
+    }
+    return m;
+}
+
+// ---- reductions ----------------------------------------------------------
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) v += __shfl_xor(v, d);
+    return v;
+}
+
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) v = fmaxf(v, __shfl_xor(v, d));
+    return v;
+}
+
+// Sum over a workgroup of T threads; `part` holds T / 64 floats.  The same
+// value, summed in the same order, on every thread.  Two calls may not share
+// `part` without a barrier between them.
+template <int T>
+__device__ __forceinline__ float block_sum(float v, float* part) {
+    v = wave_sum(v);
+    if constexpr (T == 64) return v;
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
+    __syncthreads();
+    float s = part[0];
+#pragma unroll
+    for (int w = 1; w < T / 64; ++w) s += part[w];
+    return s;
+}
+
+}  // namespace dev
+}  // namespace zero

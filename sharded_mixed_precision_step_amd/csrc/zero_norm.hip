@@ -1,0 +1,127 @@
+// Residual addition and root-mean-square norm.
+//
+// One pass over its arrays, bound by HBM: a row's elements stay in registers
+// between the reduction over the row and the outputs that need it.  A row is held by one workgroup, eight elements (one
+// 16-byte pack of a 16-bit type) per lane and step, so the workgroup size
+// follows from the row's length: one wave up to 1,024 columns, four waves at
+// 4,096.
+#include "zero_device.h"
+#include "zero_train_internal.h"
+
+namespace zero {
+namespace {
+
+using namespace dev;
+
+template <int T, int P, int XB, int RB>
+__global__ __launch_bounds__(T) void rmsnorm_kernel(const NormArgs a) {
+    __shared__ float part[T / 64];
+    const int64_t row = blockIdx.x;
+    const int t = threadIdx.x;
+    Raw8<XB> rx[P];
+    Raw8<RB == 0 ? 2 : RB> rr[P];
+    Raw8<2> w16[P];
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        const int c = (i * T + t) * 8;
+        rx[i] = load8<XB>(a.x, row * a.ld_x + c, a.cols - c);
+        if constexpr (RB != 0) rr[i] = load8<RB>(a.res, row * a.ld_r + c, a.cols - c);
+    }
+    const bool w32 = a.w_dtype == ZERO_F32;
+    if (!w32) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const int c = (i * T + t) * 8;
+            w16[i] = load8<2>(a.weight, c, a.cols - c);
+        }
+    }
+    float h[P][8];
+    float ss = 0.0f;
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        widen8<XB>(rx[i], a.x_dtype == ZERO_BF16, h[i]);
+        if constexpr (RB != 0) {
+            float r[8];
+            widen8<RB>(rr[i], a.r_dtype == ZERO_BF16, r);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) h[i][k] += r[k];
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) ss = __builtin_fmaf(h[i][k], h[i][k], ss);
+    }
+    if (a.h) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const int c = (i * T + t) * 8;
+            store8(a.h, row * a.ld_h + c, a.cols - c, a.r_dtype, h[i]);
+        }
+    }
+    ss = block_sum<T>(ss, part);
+    const float rstd = 1.0f / sqrtf(ss / static_cast<float>(a.cols) + a.eps);
+    if (a.rstd && t == 0) a.rstd[row] = rstd;
+    if (!a.y && !a.q) return;
+    const int padded = (a.cols + 127) & ~127;
+    const int blocks = padded / 128, blocks4 = (blocks + 3) & ~3;
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        const int c = (i * T + t) * 8;
+        float w[8];
+        if (w32) {
+            const Raw8<4> r = load8<4>(a.weight, c, a.cols - c);
+            widen8<4>(r, false, w);
+        } else {
+            widen8<2>(w16[i], a.w_dtype == ZERO_BF16, w);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) h[i][k] = h[i][k] * rstd * w[k];
+        // a NaN or inf rstd makes NaN of the zeros behind the row's end
+        if (c + 8 > a.cols) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (c + k >= a.cols) h[i][k] = 0.0f;
+        }
+        if (a.y) store8(a.y, row * a.ld_y + c, a.cols - c, a.y_dtype, h[i]);
+        if (a.q) {
+            // 16 neighbouring lanes hold one block of 128
+            const BlockScale s = block_scale(max16lanes(amax8(h[i])), a.fmt);
+            if (c < padded)
+                *reinterpret_cast<u32x2*>(a.q + row * a.ld_q + c) = pack8(h[i], s, a.fmt);
+            const int b = c / 128;
+            if ((t & 15) == 0 && b < blocks4)
+                a.s[row * a.ld_s + b] = static_cast<uint8_t>(b < blocks ? s.byte : 127u);
+        }
+    }
+}
+
+template <int T, int P>
+hipError_t norm_shape(const NormArgs& a, hipStream_t stream) {
+    const dim3 grid(static_cast<uint32_t>(a.rows)), block(T);
+    const bool x4 = a.x_dtype == ZERO_F32, r4 = a.r_dtype == ZERO_F32;
+    if (!a.res) {
+        if (x4) rmsnorm_kernel<T, P, 4, 0><<<grid, block, 0, stream>>>(a);
+        else rmsnorm_kernel<T, P, 2, 0><<<grid, block, 0, stream>>>(a);
+    } else if (r4) {
+        if (x4) rmsnorm_kernel<T, P, 4, 4><<<grid, block, 0, stream>>>(a);
+        else rmsnorm_kernel<T, P, 2, 4><<<grid, block, 0, stream>>>(a);
+    } else {
+        if (x4) rmsnorm_kernel<T, P, 4, 2><<<grid, block, 0, stream>>>(a);
+        else rmsnorm_kernel<T, P, 2, 2><<<grid, block, 0, stream>>>(a);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_rmsnorm(const NormArgs& a, hipStream_t stream) {
+    const int c = a.cols;
+    if (c <= 512) return norm_shape<64, 1>(a, stream);
+    if (c <= 1024) return norm_shape<64, 2>(a, stream);
+    if (c <= 2048) return norm_shape<128, 2>(a, stream);
+    if (c <= 4096) return norm_shape<256, 2>(a, stream);
+    if (c <= 8192) return norm_shape<512, 2>(a, stream);
+    if (c <= 16384) return norm_shape<1024, 2>(a, stream);
+    if (c <= 32768) return norm_shape<1024, 4>(a, stream);
+    return norm_shape<1024, 8>(a, stream);
+}
+
+}  // namespace zero

@@ -1,0 +1,245 @@
+"""The training operators' C boundary without a GPU: what every call refuses,
+before anything is enqueued, and the header against the binding."""
+import ctypes
+import math
+import os
+import re
+import subprocess
+
+import pytest
+import torch
+
+import sharded_mixed_precision_step_amd as zs
+from sharded_mixed_precision_step_amd import train
+
+pytestmark = pytest.mark.cpu
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+INCLUDE = os.path.join(ROOT, "include")
+EINVAL, EALIGN, ERANGE = -1, -2, -3
+P = 1 << 20           # fake device addresses, far apart
+A, B, C, D, E, F, G = (P * (k + 1) for k in range(7))
+
+
+def _header():
+    return re.sub(r"/\*.*?\*/", "", open(os.path.join(INCLUDE, "zero_train.h")).read(), flags=re.S)
+
+
+def test_exports_every_declared_symbol():
+    names = set(re.findall(r"\b(zero_\w+)\s*\(", _header()))
+    assert names == set(train.EXPORTED)
+    for nm in names:
+        assert hasattr(zs.lib, nm) and hasattr(zs, nm), nm
+
+
+def test_constants_and_structs_match_the_header(tmp_path):
+    text = _header()
+    for name, value in re.findall(r"#define (ZERO_\w+) (-?\d+)", text):
+        assert getattr(train, name) == int(value), name
+    fields = [f for f, _ in train.DistillInputs._fields_]
+    lines = ["#include <stddef.h>", "#include <stdio.h>", '#include "zero_train.h"',
+             "int main(void) {", 'printf("%zu\\n", sizeof(zero_distill_inputs));']
+    lines += [f'printf("%zu\\n", offsetof(zero_distill_inputs, {f}));' for f in fields]
+    src = tmp_path / "s.c"
+    src.write_text("\n".join(lines) + "\nreturn 0; }\n")
+    exe = str(tmp_path / "s")
+    subprocess.run(["gcc", "-std=c11", "-Wall", "-Wextra", "-Werror", "-I", INCLUDE, str(src),
+                    "-o", exe], check=True)
+    got = [int(x) for x in subprocess.run([exe], capture_output=True, text=True).stdout.split()]
+    assert got[0] == ctypes.sizeof(train.DistillInputs)
+    assert got[1:] == [getattr(train.DistillInputs, f).offset for f in fields]
+
+
+def _refused(rc, code, *words):
+    text = zs.lib.zero_last_error_string().decode()
+    assert rc == code, (rc, text)
+    for w in words:
+        assert w in text, text
+
+
+def _quantize(**kw):
+    a = dict(src=A, dtype=1, rows=10, cols=300, ld=300, fmt=0, q=B, ldq=384, s=C, lds=4, qt=D,
+             ldqt=128, st=E, ldst=4)
+    a.update(kw)
+    return zs.lib.zero_q8_quantize(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw,code,word", [
+    (dict(dtype=3), EINVAL, "dtype"), (dict(fmt=2), EINVAL, "fmt"), (dict(rows=-1), EINVAL, "rows"),
+    (dict(cols=-1), EINVAL, "cols"), (dict(ld=299), EINVAL, "src"), (dict(src=None), EINVAL, "src"),
+    (dict(src=A + 1), EALIGN, "src"), (dict(q=None), EINVAL, "together"),
+    (dict(st=None), EINVAL, "together"), (dict(ldq=368), EINVAL, "q"),
+    (dict(ldq=392), EALIGN, "q"), (dict(q=B + 8), EALIGN, "q"), (dict(lds=2), EALIGN, "s"),
+    (dict(lds=0), EINVAL, "s"), (dict(s=C + 2), EALIGN, "s"), (dict(ldqt=112), EINVAL, "qt"),
+    (dict(q=None, s=None, qt=None, st=None), EINVAL, "no output"),
+    (dict(q=A), EINVAL, "overlaps"), (dict(qt=B), EINVAL, "overlaps"),
+    (dict(s=B + 384 * 9 + 256), EINVAL, "overlaps"),
+    (dict(rows=1 << 40, ld=1 << 40), EINVAL, "too large"),
+    (dict(rows=1 << 39, cols=1 << 9, ld=1 << 9, ldq=1 << 9, qt=None, st=None, q=1 << 60,
+          s=1 << 61), EINVAL, "launch"),
+])
+def test_quantize_refuses(kw, code, word):
+    _refused(_quantize(**kw), code, word)
+
+
+def test_empty_calls_are_accepted_without_pointers():
+    assert _quantize(rows=0, src=None, q=None, s=None, qt=None, st=None) == 0
+    assert _quantize(cols=0, ld=0, src=None) == 0
+    assert zs.lib.zero_q8_gemm(None, 0, 128, None, 4, None, 0, 128, None, 4, 0, 5, 100, None, 1, 5,
+                               0, None) == 0
+    assert _norm(rows=0, x=None, w=None, res=None, h=None, y=None, q=None, s=None, rstd=None) == 0
+    assert _distill("zero_distill", rows=0, logits=None, index=None, teacher=None, grad=None) == 0
+
+
+def test_quantize_ctl_refuses():
+    two = (ctypes.c_void_p * 2)(A, B)
+    args = (4, 128, 128, 0, C, 128, D, 4, None, 0, None, 0)
+    call = zs.lib.zero_q8_quantize_ctl
+    _refused(call(None, *args, E, None), EINVAL, "srcs_fp16")
+    _refused(call(two, *args, None, None), EINVAL, "d_ctl")
+    _refused(call(two, *args, E + 4, None), EALIGN, "d_ctl")
+    _refused(call((ctypes.c_void_p * 2)(A, None), *args, E, None), EINVAL, "src")
+    _refused(call((ctypes.c_void_p * 2)(A, C), *args, E, None), EINVAL, "overlaps")
+
+
+def _gemm(**kw):
+    a = dict(a=A, fa=0, lda=384, sa=B, ldsa=4, b=C, fb=0, ldb=384, sb=D, ldsb=4, m=10, n=20, k=300,
+             c=E, ct=1, ldc=20, acc=0)
+    a.update(kw)
+    return zs.lib.zero_q8_gemm(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw,code,word", [
+    (dict(fa=2), EINVAL, "fmt_a"), (dict(fb=-1), EINVAL, "fmt_b"), (dict(ct=7), EINVAL, "c_dtype"),
+    (dict(m=-1), EINVAL, "m "), (dict(n=-1), EINVAL, "n "), (dict(k=-1), EINVAL, "k "),
+    (dict(acc=2), EINVAL, "accumulate"), (dict(a=None), EINVAL, "a "),
+    (dict(sb=None), EINVAL, "sb"), (dict(a=A + 4), EALIGN, "a "), (dict(lda=392), EALIGN, "a"),
+    (dict(lda=256), EINVAL, "a "), (dict(ldsa=6), EALIGN, "sa"), (dict(c=E + 1), EALIGN, "c "),
+    (dict(ldc=19), EINVAL, "c "), (dict(c=A), EINVAL, "overlaps"), (dict(c=D), EINVAL, "overlaps"),
+    (dict(k=8388609), ERANGE, "8388608"), (dict(lda=8388624), ERANGE, "8388608"),
+    (dict(m=1 << 30, n=1 << 30, ldc=1 << 30, c=1 << 62, a=1 << 50, sa=1 << 55, b=1 << 56,
+          sb=1 << 57, lda=128, ldb=128, k=1), EINVAL, ""),
+])
+def test_gemm_refuses(kw, code, word):
+    _refused(_gemm(**kw), code, word)
+
+
+def _norm(**kw):
+    a = dict(x=A, xt=1, ldx=200, res=B, rt=0, ldr=200, w=C, wt=1, rows=4, cols=200, eps=1e-5, h=D,
+             ldh=200, y=E, yt=1, ldy=200, q=F, fmt=0, ldq=256, s=G, lds=4, rstd=8 * P)
+    a.update(kw)
+    return zs.lib.zero_rmsnorm(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw,code,word", [
+    (dict(xt=5), EINVAL, "x"), (dict(rt=5), EINVAL, "residual"), (dict(wt=-1), EINVAL, "weight"),
+    (dict(yt=9), EINVAL, "y"), (dict(fmt=3), EINVAL, "fmt"), (dict(rows=-1), EINVAL, "rows"),
+    (dict(cols=0), EINVAL, "cols"), (dict(cols=65537, ldx=70000), ERANGE, "65536"),
+    (dict(eps=-1.0), EINVAL, "eps"), (dict(eps=math.nan), EINVAL, "eps"),
+    (dict(eps=math.inf), EINVAL, "eps"), (dict(s=None), EINVAL, "together"),
+    (dict(res=None), EINVAL, "residual"), (dict(x=None), EINVAL, "x "),
+    (dict(w=None), EINVAL, "weight"), (dict(ldx=199), EINVAL, "x "), (dict(x=A + 1), EALIGN, "x "),
+    (dict(res=B + 2), EALIGN, "residual"), (dict(ldq=240), EINVAL, "q "),
+    (dict(rstd=8 * P + 2), EALIGN, "rstd"), (dict(h=A), EINVAL, "overlaps"),
+    (dict(h=B, ldh=201), EINVAL, "overlaps"), (dict(y=A, yt=0), EINVAL, "overlaps"),
+    (dict(y=B), EINVAL, "overlaps"), (dict(y=C), EINVAL, "overlaps"),
+    (dict(y=D), EINVAL, "overlaps"), (dict(q=A), EINVAL, "overlaps"),
+    (dict(h=None, y=None, q=None, s=None, rstd=None), EINVAL, "no output"),
+])
+def test_norm_refuses(kw, code, word):
+    _refused(_norm(**kw), code, word)
+
+
+def _back(**kw):
+    a = dict(dy=A, dt=1, ldd=200, h=B, ht=0, ldh=200, w=C, wt=1, rstd=D, dr=E, drt=1, ldr=200,
+             rows=4, cols=200, dx=F, dxt=1, ldx=200, dw=G, dwt=1, ws=8 * P, nws=4 * 4 * 200)
+    a.update(kw)
+    return zs.lib.zero_rmsnorm_backward(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw,code,word", [
+    (dict(dt=4), EINVAL, "dy"), (dict(ht=4), EINVAL, "h"), (dict(wt=4), EINVAL, "weight"),
+    (dict(drt=4), EINVAL, "dresidual"), (dict(dxt=4), EINVAL, "dx"), (dict(dwt=4), EINVAL, "dw"),
+    (dict(rows=-2), EINVAL, "rows"), (dict(cols=0), EINVAL, "cols"),
+    (dict(cols=70000), ERANGE, "65536"), (dict(rstd=None), EINVAL, "rstd"),
+    (dict(dx=None), EINVAL, "dx"), (dict(ldh=10), EINVAL, "h "), (dict(nws=3199), ERANGE, "3200"),
+    (dict(ws=None), EINVAL, "workspace"), (dict(ws=8 * P + 4), EALIGN, "workspace"),
+    (dict(dx=A, ldx=201), EINVAL, "overlaps"), (dict(dx=B), EINVAL, "overlaps"),
+    (dict(dx=D), EINVAL, "overlaps"), (dict(dw=C), EINVAL, "overlaps"),
+    (dict(ws=A), EINVAL, "overlaps"), (dict(dw=F), EINVAL, "overlaps"),
+])
+def test_norm_backward_refuses(kw, code, word):
+    _refused(_back(**kw), code, word)
+
+
+def test_norm_backward_workspace():
+    f = zs.zero_rmsnorm_backward_workspace
+    assert f(0, 100) == 0 and f(4, 200) == 3200 and 0 < f(10 ** 9, 65536) <= 4 * 1024 * 65536
+    for rows, cols in ((-1, 5), (5, 0), (5, 65537)):
+        with pytest.raises(zs.ZeroStepError):
+            f(rows, cols)
+
+
+def _distill(name, rows=4, vocab=100, ld=100, top=5, ldt=5, dt=1, tt=0, ib=4, tau=1.0, logits=A,
+             index=B, teacher=C, weight=D, loss=E, lse=F, grad=G, ldg=100, S=1.0, ctl=None):
+    i = train.DistillInputs(logits, index, teacher, weight, rows, vocab, ld, ldt, dt, tt, ib, top,
+                            tau, 0)
+    r = ctypes.byref(i)
+    if name == "zero_distill_forward":
+        return zs.lib.zero_distill_forward(r, loss, lse, None)
+    if name == "zero_distill_backward":
+        return zs.lib.zero_distill_backward(r, lse, S, ctl, grad, ldg, None)
+    return zs.lib.zero_distill(r, S, ctl, loss, lse, grad, ldg, None)
+
+
+NAMES = ["zero_distill_forward", "zero_distill_backward", "zero_distill"]
+
+
+@pytest.mark.parametrize("name", NAMES)
+@pytest.mark.parametrize("kw,code,word", [
+    (dict(dt=3), EINVAL, "logits_dtype"), (dict(tt=3), EINVAL, "top_dtype"),
+    (dict(ib=2), EINVAL, "index_bytes"), (dict(rows=-1), EINVAL, "rows"),
+    (dict(vocab=0), EINVAL, "vocab"), (dict(vocab=1 << 31, ld=1 << 31), EINVAL, "vocab"),
+    (dict(top=0), EINVAL, "top"), (dict(top=1025, ldt=1025), ERANGE, "1024"),
+    (dict(tau=0.0), EINVAL, "temperature"), (dict(tau=math.nan), EINVAL, "temperature"),
+    (dict(tau=math.inf), EINVAL, "temperature"), (dict(tau=1e-39), EINVAL, "temperature"),
+    (dict(tau=1e30), EINVAL, "temperature"), (dict(ld=99), EINVAL, "logits"),
+    (dict(ldt=4), EINVAL, "top_index"), (dict(logits=None), EINVAL, "logits"),
+    (dict(index=None), EINVAL, "top_index"), (dict(teacher=None), EINVAL, "top_logit"),
+    (dict(logits=A + 1), EALIGN, "logits"), (dict(index=B + 2), EALIGN, "top_index"),
+    (dict(ib=8, index=B + 4), EALIGN, "top_index"), (dict(weight=D + 1), EALIGN, "row_weight"),
+])
+def test_distill_refuses(name, kw, code, word):
+    _refused(_distill(name, **kw), code, word)
+
+
+@pytest.mark.parametrize("name", NAMES[1:])
+@pytest.mark.parametrize("kw,code,word", [
+    (dict(S=0.0), EINVAL, "loss_scale"), (dict(S=math.inf), EINVAL, "loss_scale"),
+    (dict(ctl=8 * P + 4), EALIGN, "d_ctl"), (dict(grad=None), EINVAL, "grad"),
+    (dict(ldg=99), EINVAL, "grad"), (dict(grad=A, ldg=101), EINVAL, "stride"),
+    (dict(grad=A + 2), EINVAL, "overlaps"), (dict(grad=B), EINVAL, "overlaps"),
+])
+def test_distill_gradient_refuses(name, kw, code, word):
+    _refused(_distill(name, **kw), code, word)
+
+
+def test_distill_outputs_refused():
+    _refused(_distill(NAMES[0], loss=None, lse=None), EINVAL, "no output")
+    _refused(_distill(NAMES[0], loss=A), EINVAL, "overlaps")
+    _refused(_distill(NAMES[0], loss=F), EINVAL, "overlaps")
+    _refused(_distill(NAMES[1], lse=None), EINVAL, "lse")
+    _refused(_distill(NAMES[2], lse=G + 4), EINVAL, "overlaps")
+
+
+def test_the_binding_refuses_host_and_mismatched_tensors():
+    x, w = torch.zeros(4, 200), torch.ones(200)
+    with pytest.raises(TypeError):
+        zs.zero_rmsnorm(x, w, 1e-5, y=torch.empty_like(x))
+    with pytest.raises(TypeError):
+        zs.zero_q8_quantize(x, *zs.q8_empty(4, 200, device="cpu"))
+    with pytest.raises(TypeError):
+        zs.zero_distill_forward(x, torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2),
+                                torch.zeros(4), None)
+    assert zs.q8_shape(5, 0) == ((5, 0), (5, 0))
+    assert zs.q8_shape(5, 129) == ((5, 256), (5, 4)) and zs.q8_shape(1, 640) == ((1, 640), (1, 8))
