@@ -186,6 +186,30 @@ def test_gemm_is_the_product(m, n, k, fa, fb):
         ref.assert_close(got, live, tol, f"c {dtype}")
 
 
+@pytest.mark.parametrize("m,n,steps", [(2100, 4200, s) for s in (6, 7, 8, 9)] +
+                         [(2000, 4000, s) for s in (1, 2, 3, 4)] +
+                         [(1000, 4000, s) for s in (7, 8, 9, 10)] +
+                         [(520, 1030, s) for s in (1, 2, 3, 5, 8)] + [(9, 4096, s) for s in (1, 33)])
+def test_gemm_of_every_tile_and_step_count(m, n, steps):
+    """Sizes at which each of the kernel's tiles is the chosen one, with ragged
+    edges, at every remainder of its loops over k."""
+    dev = device()
+    k = 128 * steps - 5
+    print(f"case: gemm {m}x{n}x{k}", flush=True)
+    a, sa = _operand(m, k, E5, m, dev)
+    b, sb = _operand(n, k, E4, n, dev)
+    va, vb = ref.from_blocks(a, sa), ref.from_blocks(b, sb)
+    want = va @ vb.t()
+    tol = _gemm_tol(va, vb, sa, sb, torch.bfloat16, want)
+    c = torch.full((m, n), 7.0, dtype=torch.bfloat16, device=dev)
+    zs.zero_q8_gemm(a, sa, b, sb, c)
+    ref.assert_close(c, want, tol, "c")
+    ones = torch.ones(m, n, device=dev)
+    zs.zero_q8_gemm(a, sa, b, sb, ones, accumulate=True)
+    tol = _gemm_tol(va, vb, sa, sb, torch.float32, want + 1, torch.ones_like(want))
+    ref.assert_close(ones, want + 1, tol, "added to c")
+
+
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("m,n,k", [(3, 50, 300), (140, 270, 512), (700, 515, 256)])
 def test_gemm_accumulates_into_a_strided_c(m, n, k, dtype):
