@@ -73,80 +73,95 @@ def _declare() -> None:
 _declare()
 
 
-class _Call:
-    """The device of one call: every tensor is on it, and it is current while
-    the library enqueues."""
+# What a call looks at is written out below rather than wrapped in objects: a
+# short call's time is the host's.
 
-    def __init__(self, device: torch.device):
-        if device.type != "cuda":
-            raise TypeError("the tensors must be device tensors")
-        self.device = device
-
-    def mat(self, t: torch.Tensor, kinds: dict, name: str) -> Tuple[int, int, int]:
-        """(pointer, type code, row stride) of a matrix."""
-        code = kinds.get(t.dtype)
-        if code is None:
-            raise TypeError(f"{name} has dtype {t.dtype}")
-        if t.device != self.device:
-            raise TypeError(f"{name} is on {t.device}, expected {self.device}")
-        if t.dim() != 2:
-            raise ValueError(f"{name} has {t.dim()} dimensions, expected 2")
+def _mat(t: torch.Tensor, kinds: dict, dev: torch.device, name: str) -> Tuple[int, int, int]:
+    """(pointer, type code, row stride) of a matrix on dev."""
+    code = kinds.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} has dtype {t.dtype}")
+    if t.device != dev:
+        raise TypeError(f"{name} is on {t.device}, expected {dev}")
+    stride = t.stride()
+    if len(stride) != 2:
+        raise ValueError(f"{name} has {len(stride)} dimensions, expected 2")
+    ld, inner = stride
+    if inner != 1 or ld < t.shape[1]:
         rows, cols = t.shape
-        ld, inner = t.stride()
         if inner != 1 and cols > 1:
             raise ValueError(f"the rows of {name} are not contiguous")
-        return t.data_ptr(), code, ld if rows > 1 else max(ld, cols)
+        if rows <= 1:
+            ld = max(ld, cols)
+    return t.data_ptr(), code, ld
 
-    def like(self, t: torch.Tensor, shape, kinds: dict, name: str) -> Tuple[int, int, int]:
-        if tuple(t.shape) != tuple(shape):
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-        return self.mat(t, kinds, name)
 
-    def vec(self, t: torch.Tensor, n: int, kinds: dict, name: str) -> Tuple[int, int]:
-        """(pointer, type code) of a contiguous vector of n elements."""
-        code = kinds.get(t.dtype)
-        if code is None:
-            raise TypeError(f"{name} has dtype {t.dtype}")
-        if t.device != self.device:
-            raise TypeError(f"{name} is on {t.device}, expected {self.device}")
-        if t.numel() != n:
-            raise ValueError(f"{name} has {t.numel()} elements, expected {n}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        return t.data_ptr(), code
+def _like(t: torch.Tensor, shape, kinds: dict, dev: torch.device, name: str):
+    """_mat of a matrix of this shape."""
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    return _mat(t, kinds, dev, name)
 
-    def q8(self, data: Optional[torch.Tensor], scales: Optional[torch.Tensor], rows: int,
-           cols: int, name: str, fmt: Optional[int] = None):
-        """(data pointer, ld, scale pointer, ld, format) of a q8 matrix."""
-        if data is None or scales is None:
-            if data is not None or scales is not None:
-                raise ValueError(f"{name}: data and scales go together")
-            return None, 0, None, 0, fmt
-        blocks = -(-cols // ZERO_Q8_BLOCK)
-        p, code, ld = self.mat(data, _FP8, name)
-        if fmt is not None and code != fmt:
-            raise TypeError(f"{name} has dtype {data.dtype}, unlike the other output")
-        ps, _, lds = self.mat(scales, _SCALE, f"scales of {name}")
-        if data.shape[0] != rows or data.shape[1] < blocks * ZERO_Q8_BLOCK:
-            raise ValueError(f"{name} has shape {tuple(data.shape)}, expected {rows} rows of "
-                             f"{blocks * ZERO_Q8_BLOCK}")
-        if scales.shape[0] != rows or scales.shape[1] < -(-blocks // 4) * 4:
-            raise ValueError(f"scales of {name} have shape {tuple(scales.shape)}, expected "
-                             f"{rows} rows of {-(-blocks // 4) * 4}")
-        return p, ld, ps, lds, code
 
-    def run(self, fn, *args, stream) -> None:
-        if stream is None:
-            stream = torch.cuda.current_stream(self.device).cuda_stream
-        elif isinstance(stream, torch.cuda.Stream):
-            stream = stream.cuda_stream
-        if self.device.index == torch.cuda.current_device():
-            rc = fn(*args, stream)
-        else:
-            with torch.cuda.device(self.device):
-                rc = fn(*args, stream)
-        if rc:
-            _check(rc)
+def _vec(t: torch.Tensor, n: int, kinds: dict, dev: torch.device, name: str) -> Tuple[int, int]:
+    """(pointer, type code) of a contiguous vector of n elements on dev."""
+    code = kinds.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} has dtype {t.dtype}")
+    if t.device != dev:
+        raise TypeError(f"{name} is on {t.device}, expected {dev}")
+    if t.numel() != n:
+        raise ValueError(f"{name} has {t.numel()} elements, expected {n}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr(), code
+
+
+def _q8(data: Optional[torch.Tensor], scales: Optional[torch.Tensor], rows: int, cols: int,
+        dev: torch.device, name: str, fmt: Optional[int] = None):
+    """(data pointer, ld, scale pointer, ld, format) of a q8 matrix."""
+    if data is None or scales is None:
+        if data is not None or scales is not None:
+            raise ValueError(f"{name}: data and scales go together")
+        return None, 0, None, 0, fmt
+    p, code, ld = _mat(data, _FP8, dev, name)
+    if fmt is not None and code != fmt:
+        raise TypeError(f"{name} has dtype {data.dtype}, unlike the other output")
+    ps, _, lds = _mat(scales, _SCALE, dev, name)
+    blocks = -(-cols // ZERO_Q8_BLOCK)
+    have, wide = data.shape
+    if have != rows or wide < blocks * ZERO_Q8_BLOCK:
+        raise ValueError(f"{name} has shape {tuple(data.shape)}, expected {rows} rows of "
+                         f"{blocks * ZERO_Q8_BLOCK}")
+    have, wide = scales.shape
+    if have != rows or wide < -(-blocks // 4) * 4:
+        raise ValueError(f"scales of {name} have shape {tuple(scales.shape)}, expected "
+                         f"{rows} rows of {-(-blocks // 4) * 4}")
+    return p, ld, ps, lds, code
+
+
+def _device(t: torch.Tensor) -> torch.device:
+    dev = t.device
+    if dev.type != "cuda":
+        raise TypeError("the tensors must be device tensors")
+    return dev
+
+
+def _raw_stream(stream, dev: torch.device) -> int:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev.index)
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
+def _run(fn, dev: torch.device, *args) -> None:
+    """Make the call with dev current, as the library launches there."""
+    if dev.index == torch.cuda.current_device():
+        rc = fn(*args)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args)
+    if rc:
+        _check(rc)
 
 
 _F32 = {torch.float32: ZERO_F32}
@@ -172,13 +187,13 @@ def zero_q8_quantize(src: torch.Tensor, q: Optional[torch.Tensor] = None,
     """src [rows, cols] in the q8 layout, by rows into (q, s), transposed into
     (qt, st), or both; the 8-bit format is the outputs' dtype (see
     zero_train.h)."""
-    call = _Call(src.device)
-    p, dt, ld = call.mat(src, _ELEM, "src")
+    dev = _device(src)
+    p, dt, ld = _mat(src, _ELEM, dev, "src")
     rows, cols = src.shape
-    pq, ldq, ps, lds, fmt = call.q8(q, s, rows, cols, "q")
-    pt, ldt, pst, ldst, fmt = call.q8(qt, st, cols, rows, "qt", fmt)
-    call.run(lib.zero_q8_quantize, p, dt, rows, cols, ld, ZERO_E4M3 if fmt is None else fmt, pq,
-             ldq, ps, lds, pt, ldt, pst, ldst, stream=stream)
+    pq, ldq, ps, lds, fmt = _q8(q, s, rows, cols, dev, "q")
+    pt, ldt, pst, ldst, fmt = _q8(qt, st, cols, rows, dev, "qt", fmt)
+    _run(lib.zero_q8_quantize, dev, p, dt, rows, cols, ld, ZERO_E4M3 if fmt is None else fmt, pq,
+         ldq, ps, lds, pt, ldt, pst, ldst, _raw_stream(stream, dev))
 
 
 def zero_q8_quantize_ctl(srcs_fp16, ctl: torch.Tensor, q: Optional[torch.Tensor] = None,
@@ -187,20 +202,20 @@ def zero_q8_quantize_ctl(srcs_fp16, ctl: torch.Tensor, q: Optional[torch.Tensor]
     """zero_q8_quantize of the copy the control block says is current: srcs_fp16
     are the same fp16 matrix in the two copies of the parameters."""
     first, second = srcs_fp16
-    call = _Call(first.device)
+    dev = _device(first)
     rows, cols = first.shape
     half = {torch.float16: ZERO_F16}
-    p0, _, ld = call.mat(first, half, "srcs_fp16[0]")
-    p1, _, ld1 = call.like(second, (rows, cols), half, "srcs_fp16[1]")
+    p0, _, ld = _mat(first, half, dev, "srcs_fp16[0]")
+    p1, _, ld1 = _like(second, (rows, cols), half, dev, "srcs_fp16[1]")
     if ld1 != ld:
         raise ValueError("the two copies have different row strides")
-    if ctl.device != call.device:
-        raise TypeError(f"ctl is on {ctl.device}, expected {call.device}")
-    pq, ldq, ps, lds, fmt = call.q8(q, s, rows, cols, "q")
-    pt, ldt, pst, ldst, fmt = call.q8(qt, st, cols, rows, "qt", fmt)
-    call.run(lib.zero_q8_quantize_ctl, (ctypes.c_void_p * 2)(p0, p1), rows, cols, ld,
-             ZERO_E4M3 if fmt is None else fmt, pq, ldq, ps, lds, pt, ldt, pst, ldst, _ctl(ctl),
-             stream=stream)
+    if ctl.device != dev:
+        raise TypeError(f"ctl is on {ctl.device}, expected {dev}")
+    pq, ldq, ps, lds, fmt = _q8(q, s, rows, cols, dev, "q")
+    pt, ldt, pst, ldst, fmt = _q8(qt, st, cols, rows, dev, "qt", fmt)
+    _run(lib.zero_q8_quantize_ctl, dev, (ctypes.c_void_p * 2)(p0, p1), rows, cols, ld,
+         ZERO_E4M3 if fmt is None else fmt, pq, ldq, ps, lds, pt, ldt, pst, ldst, _ctl(ctl),
+         _raw_stream(stream, dev))
 
 
 def zero_q8_gemm(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb: torch.Tensor,
@@ -208,17 +223,17 @@ def zero_q8_gemm(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb: torch.T
                  stream=None) -> None:
     """c [m, n] = a b^T of q8 matrices a [m, k] and b [n, k] (added to c with
     ``accumulate``).  k defaults to a's padded row length."""
-    call = _Call(c.device)
-    pc, dt, ldc = call.mat(c, _ELEM, "c")
+    dev = _device(c)
+    pc, dt, ldc = _mat(c, _ELEM, dev, "c")
     m, n = c.shape
     if k is None:
         k = a.shape[1]
         if b.shape[1] != k:
             raise ValueError(f"a has rows of {k}, b of {b.shape[1]}")
-    pa, lda, psa, ldsa, fa = call.q8(a, sa, m, k, "a")
-    pb, ldb, psb, ldsb, fb = call.q8(b, sb, n, k, "b")
-    call.run(lib.zero_q8_gemm, pa, fa, lda, psa, ldsa, pb, fb, ldb, psb, ldsb, m, n, k, pc, dt,
-             ldc, 1 if accumulate else 0, stream=stream)
+    pa, lda, psa, ldsa, fa = _q8(a, sa, m, k, dev, "a")
+    pb, ldb, psb, ldsb, fb = _q8(b, sb, n, k, dev, "b")
+    _run(lib.zero_q8_gemm, dev, pa, fa, lda, psa, ldsa, pb, fb, ldb, psb, ldsb, m, n, k, pc, dt,
+         ldc, 1 if accumulate else 0, _raw_stream(stream, dev))
 
 
 def zero_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float, *,
@@ -229,22 +244,22 @@ def zero_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float, *,
     """h = x + residual; y = h / sqrt(mean(h^2) + eps) * weight, into y, or in
     the q8 layout into (q, s), or both; rstd and the rounded h for the
     backward pass (see zero_train.h)."""
-    call = _Call(x.device)
-    px, dx, ldx = call.mat(x, _ELEM, "x")
+    dev = _device(x)
+    px, dx, ldx = _mat(x, _ELEM, dev, "x")
     rows, cols = shape = x.shape
-    pw, dw = call.vec(weight, cols, _ELEM, "weight")
+    pw, dw = _vec(weight, cols, _ELEM, dev, "weight")
     pr, dr, ldr = (None, ZERO_F32, 0) if residual is None else \
-        call.like(residual, shape, _ELEM, "residual")
+        _like(residual, shape, _ELEM, dev, "residual")
     ph, ldh = None, 0
     if h is not None:
         if residual is not None and h.dtype != residual.dtype:
             raise TypeError(f"h has dtype {h.dtype}, residual {residual.dtype}")
-        ph, _, ldh = call.like(h, shape, _ELEM, "h")
-    py, dy, ldy = (None, ZERO_F32, 0) if y is None else call.like(y, shape, _ELEM, "y")
-    pq, ldq, ps, lds, fmt = call.q8(q, s, rows, cols, "q")
-    prstd = None if rstd is None else call.vec(rstd, rows, _F32, "rstd")[0]
-    call.run(lib.zero_rmsnorm, px, dx, ldx, pr, dr, ldr, pw, dw, rows, cols, eps, ph, ldh, py, dy,
-             ldy, pq, fmt or ZERO_E4M3, ldq, ps, lds, prstd, stream=stream)
+        ph, _, ldh = _like(h, shape, _ELEM, dev, "h")
+    py, dy, ldy = (None, ZERO_F32, 0) if y is None else _like(y, shape, _ELEM, dev, "y")
+    pq, ldq, ps, lds, fmt = _q8(q, s, rows, cols, dev, "q")
+    prstd = None if rstd is None else _vec(rstd, rows, _F32, dev, "rstd")[0]
+    _run(lib.zero_rmsnorm, dev, px, dx, ldx, pr, dr, ldr, pw, dw, rows, cols, eps, ph, ldh, py, dy,
+         ldy, pq, fmt or ZERO_E4M3, ldq, ps, lds, prstd, _raw_stream(stream, dev))
 
 
 def zero_rmsnorm_backward_workspace(rows: int, cols: int) -> int:
@@ -262,47 +277,47 @@ def zero_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tenso
     """dx (of x and of residual, with dres, the gradient at h, added) and dw;
     workspace: uint8, zero_rmsnorm_backward_workspace bytes, not needed when
     dw is None (see zero_train.h)."""
-    call = _Call(dy.device)
-    pd, dd, ldd = call.mat(dy, _ELEM, "dy")
+    dev = _device(dy)
+    pd, dd, ldd = _mat(dy, _ELEM, dev, "dy")
     rows, cols = shape = dy.shape
-    ph, dh, ldh = call.like(h, shape, _ELEM, "h")
-    pw, dwt = call.vec(weight, cols, _ELEM, "weight")
-    prstd, _ = call.vec(rstd, rows, _F32, "rstd")
-    pr, dr, ldr = (None, ZERO_F32, 0) if dres is None else call.like(dres, shape, _ELEM, "dres")
-    px, dxt, ldx = call.like(dx, shape, _ELEM, "dx")
-    pdw, ddw = (None, ZERO_F32) if dw is None else call.vec(dw, cols, _ELEM, "dw")
+    ph, dh, ldh = _like(h, shape, _ELEM, dev, "h")
+    pw, dwt = _vec(weight, cols, _ELEM, dev, "weight")
+    prstd, _ = _vec(rstd, rows, _F32, dev, "rstd")
+    pr, dr, ldr = (None, ZERO_F32, 0) if dres is None else _like(dres, shape, _ELEM, dev, "dres")
+    px, dxt, ldx = _like(dx, shape, _ELEM, dev, "dx")
+    pdw, ddw = (None, ZERO_F32) if dw is None else _vec(dw, cols, _ELEM, dev, "dw")
     pws, nws = (None, 0) if workspace is None else \
-        (call.vec(workspace, workspace.numel(), _BYTES, "workspace")[0], workspace.numel())
-    call.run(lib.zero_rmsnorm_backward, pd, dd, ldd, ph, dh, ldh, pw, dwt, prstd, pr, dr, ldr,
-             rows, cols, px, dxt, ldx, pdw, ddw, pws, nws, stream=stream)
+        (_vec(workspace, workspace.numel(), _BYTES, dev, "workspace")[0], workspace.numel())
+    _run(lib.zero_rmsnorm_backward, dev, pd, dd, ldd, ph, dh, ldh, pw, dwt, prstd, pr, dr, ldr,
+         rows, cols, px, dxt, ldx, pdw, ddw, pws, nws, _raw_stream(stream, dev))
 
 
-def _distill_inputs(call: _Call, logits, index, teacher, temperature, row_weight):
-    p, dt, ld = call.mat(logits, _ELEM, "logits")
+def _distill_inputs(dev: torch.device, logits, index, teacher, temperature, row_weight):
+    p, dt, ld = _mat(logits, _ELEM, dev, "logits")
     rows, vocab = logits.shape
     if index.dim() != 2:
         raise ValueError(f"index has {index.dim()} dimensions, expected 2")
     top = index.shape[1]
-    pi, ib, ldi = call.like(index, (rows, top), _INDEX, "index")
-    pt, tt, ldt = call.like(teacher, (rows, top), _ELEM, "teacher")
+    pi, ib, ldi = _like(index, (rows, top), _INDEX, dev, "index")
+    pt, tt, ldt = _like(teacher, (rows, top), _ELEM, dev, "teacher")
     if ldi != ldt:
         raise ValueError("index and teacher have different row strides")
-    pw = None if row_weight is None else call.vec(row_weight, rows, _F32, "row_weight")[0]
+    pw = None if row_weight is None else _vec(row_weight, rows, _F32, dev, "row_weight")[0]
     return DistillInputs(p, pi, pt, pw, rows, vocab, ld, ldi, dt, tt, ib, top, temperature, 0)
 
 
-def _distill_scale(call: _Call, ctl):
+def _distill_scale(dev: torch.device, ctl):
     if ctl is None:
         return None
-    if ctl.device != call.device:
-        raise TypeError(f"ctl is on {ctl.device}, expected {call.device}")
+    if ctl.device != dev:
+        raise TypeError(f"ctl is on {ctl.device}, expected {dev}")
     return _ctl(ctl)
 
 
-def _distill_grad(call: _Call, grad, logits):
+def _distill_grad(dev: torch.device, grad, logits):
     if grad.dtype != logits.dtype:
         raise TypeError(f"grad has dtype {grad.dtype}, logits {logits.dtype}")
-    p, _, ld = call.like(grad, logits.shape, _ELEM, "grad")
+    p, _, ld = _like(grad, logits.shape, _ELEM, dev, "grad")
     return p, ld
 
 
@@ -313,12 +328,12 @@ def zero_distill_forward(logits: torch.Tensor, index: torch.Tensor, teacher: tor
     """Per-row loss and lse (fp32[rows]) of the student's logits [rows, vocab]
     against the teacher's entries: vocab indices [rows, top] (-1: no entry) and
     logits [rows, top] (see zero_distill_inputs in zero_train.h)."""
-    call = _Call(logits.device)
+    dev = _device(logits)
     rows = logits.shape[0]
-    inputs = _distill_inputs(call, logits, index, teacher, temperature, row_weight)
-    pl = None if loss is None else call.vec(loss, rows, _F32, "loss")[0]
-    pe = None if lse is None else call.vec(lse, rows, _F32, "lse")[0]
-    call.run(lib.zero_distill_forward, ctypes.byref(inputs), pl, pe, stream=stream)
+    inputs = _distill_inputs(dev, logits, index, teacher, temperature, row_weight)
+    pl = None if loss is None else _vec(loss, rows, _F32, dev, "loss")[0]
+    pe = None if lse is None else _vec(lse, rows, _F32, dev, "lse")[0]
+    _run(lib.zero_distill_forward, dev, ctypes.byref(inputs), pl, pe, _raw_stream(stream, dev))
 
 
 def zero_distill_backward(logits: torch.Tensor, index: torch.Tensor, teacher: torch.Tensor,
@@ -327,12 +342,12 @@ def zero_distill_backward(logits: torch.Tensor, index: torch.Tensor, teacher: to
                           ctl: Optional[torch.Tensor] = None, stream=None) -> None:
     """The loss-scaled gradient of the logits, from the forward's lse.  S is
     loss_scale, or the scale of the control block ``ctl``; grad may be logits."""
-    call = _Call(logits.device)
-    inputs = _distill_inputs(call, logits, index, teacher, temperature, row_weight)
-    pe = call.vec(lse, logits.shape[0], _F32, "lse")[0]
-    pg, ldg = _distill_grad(call, grad, logits)
-    call.run(lib.zero_distill_backward, ctypes.byref(inputs), pe, loss_scale,
-             _distill_scale(call, ctl), pg, ldg, stream=stream)
+    dev = _device(logits)
+    inputs = _distill_inputs(dev, logits, index, teacher, temperature, row_weight)
+    pe = _vec(lse, logits.shape[0], _F32, dev, "lse")[0]
+    pg, ldg = _distill_grad(dev, grad, logits)
+    _run(lib.zero_distill_backward, dev, ctypes.byref(inputs), pe, loss_scale,
+         _distill_scale(dev, ctl), pg, ldg, _raw_stream(stream, dev))
 
 
 def zero_distill(logits: torch.Tensor, index: torch.Tensor, teacher: torch.Tensor,
@@ -341,11 +356,11 @@ def zero_distill(logits: torch.Tensor, index: torch.Tensor, teacher: torch.Tenso
                  loss_scale: float = 1.0, ctl: Optional[torch.Tensor] = None,
                  stream=None) -> None:
     """zero_distill_forward and zero_distill_backward in one pass."""
-    call = _Call(logits.device)
+    dev = _device(logits)
     rows = logits.shape[0]
-    inputs = _distill_inputs(call, logits, index, teacher, temperature, row_weight)
-    pl = None if loss is None else call.vec(loss, rows, _F32, "loss")[0]
-    pe = None if lse is None else call.vec(lse, rows, _F32, "lse")[0]
-    pg, ldg = _distill_grad(call, grad, logits)
-    call.run(lib.zero_distill, ctypes.byref(inputs), loss_scale, _distill_scale(call, ctl), pl, pe,
-             pg, ldg, stream=stream)
+    inputs = _distill_inputs(dev, logits, index, teacher, temperature, row_weight)
+    pl = None if loss is None else _vec(loss, rows, _F32, dev, "loss")[0]
+    pe = None if lse is None else _vec(lse, rows, _F32, dev, "lse")[0]
+    pg, ldg = _distill_grad(dev, grad, logits)
+    _run(lib.zero_distill, dev, ctypes.byref(inputs), loss_scale, _distill_scale(dev, ctl), pl, pe,
+         pg, ldg, _raw_stream(stream, dev))
