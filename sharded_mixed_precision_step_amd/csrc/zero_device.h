@@ -217,18 +217,17 @@ __device__ __forceinline__ float wave_max(float v) {
     return v;
 }
 
-// Sum over a workgroup of T threads; `part` holds T / 64 floats.  The same
-// value, summed in the same order, on every thread.  Two calls may not share
-// `part` without a barrier between them.
-template <int T>
+// Sum over a workgroup of up to 1,024 threads, whole waves; `part` holds a float
+// per wave.  The same value, summed in the same order, on every thread.  Two
+// calls may not share `part` without a barrier between them.
 __device__ __forceinline__ float block_sum(float v, float* part) {
     v = wave_sum(v);
-    if constexpr (T == 64) return v;
+    const int waves = static_cast<int>(blockDim.x >> 6);
+    if (waves == 1) return v;
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
     __syncthreads();
     float s = part[0];
-#pragma unroll
-    for (int w = 1; w < T / 64; ++w) s += part[w];
+    for (int w = 1; w < waves; ++w) s += part[w];
     return s;
 }
 

@@ -55,7 +55,7 @@ __device__ __forceinline__ float block_max(float v, float* part) {
 
 __device__ __forceinline__ float block_add(float v, float* part) {
     __syncthreads();
-    return block_sum<kT>(v, part);
+    return block_sum(v, part);
 }
 
 template <int B, DistillMode MODE>

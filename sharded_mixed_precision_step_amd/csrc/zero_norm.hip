@@ -13,9 +13,10 @@ namespace {
 
 using namespace dev;
 
-template <int T, int P, int XB, int RB>
-__global__ __launch_bounds__(T) void rmsnorm_kernel(const NormArgs a) {
-    __shared__ float part[T / 64];
+template <int MAX_T, int P, int XB, int RB>
+__global__ __launch_bounds__(MAX_T) void rmsnorm_kernel(const NormArgs a) {
+    __shared__ float part[16];
+    const int T = static_cast<int>(blockDim.x);
     const int64_t row = blockIdx.x;
     const int t = threadIdx.x;
     Raw8<XB> rx[P];
@@ -56,7 +57,7 @@ __global__ __launch_bounds__(T) void rmsnorm_kernel(const NormArgs a) {
             store8(a.h, row * a.ld_h + c, a.cols - c, a.r_dtype, h[i]);
         }
     }
-    ss = block_sum<T>(ss, part);
+    ss = block_sum(ss, part);
     const float rstd = 1.0f / sqrtf(ss / static_cast<float>(a.cols) + a.eps);
     if (a.rstd && t == 0) a.rstd[row] = rstd;
     if (!a.y && !a.q) return;
@@ -93,19 +94,20 @@ __global__ __launch_bounds__(T) void rmsnorm_kernel(const NormArgs a) {
     }
 }
 
-template <int T, int P>
+template <int MAX_T, int P>
 hipError_t norm_shape(const NormArgs& a, hipStream_t stream) {
-    const dim3 grid(static_cast<uint32_t>(a.rows)), block(T);
+    const dim3 grid(static_cast<uint32_t>(a.rows));
+    const dim3 block(static_cast<uint32_t>((a.cols + P * 512 - 1) / (P * 512) * 64));
     const bool x4 = a.x_dtype == ZERO_F32, r4 = a.r_dtype == ZERO_F32;
     if (!a.res) {
-        if (x4) rmsnorm_kernel<T, P, 4, 0><<<grid, block, 0, stream>>>(a);
-        else rmsnorm_kernel<T, P, 2, 0><<<grid, block, 0, stream>>>(a);
+        if (x4) rmsnorm_kernel<MAX_T, P, 4, 0><<<grid, block, 0, stream>>>(a);
+        else rmsnorm_kernel<MAX_T, P, 2, 0><<<grid, block, 0, stream>>>(a);
     } else if (r4) {
-        if (x4) rmsnorm_kernel<T, P, 4, 4><<<grid, block, 0, stream>>>(a);
-        else rmsnorm_kernel<T, P, 2, 4><<<grid, block, 0, stream>>>(a);
+        if (x4) rmsnorm_kernel<MAX_T, P, 4, 4><<<grid, block, 0, stream>>>(a);
+        else rmsnorm_kernel<MAX_T, P, 2, 4><<<grid, block, 0, stream>>>(a);
     } else {
-        if (x4) rmsnorm_kernel<T, P, 4, 2><<<grid, block, 0, stream>>>(a);
-        else rmsnorm_kernel<T, P, 2, 2><<<grid, block, 0, stream>>>(a);
+        if (x4) rmsnorm_kernel<MAX_T, P, 4, 2><<<grid, block, 0, stream>>>(a);
+        else rmsnorm_kernel<MAX_T, P, 2, 2><<<grid, block, 0, stream>>>(a);
     }
     return hipGetLastError();
 }
@@ -115,10 +117,6 @@ hipError_t norm_shape(const NormArgs& a, hipStream_t stream) {
 hipError_t launch_rmsnorm(const NormArgs& a, hipStream_t stream) {
     const int c = a.cols;
     if (c <= 512) return norm_shape<64, 1>(a, stream);
-    if (c <= 1024) return norm_shape<64, 2>(a, stream);
-    if (c <= 2048) return norm_shape<128, 2>(a, stream);
-    if (c <= 4096) return norm_shape<256, 2>(a, stream);
-    if (c <= 8192) return norm_shape<512, 2>(a, stream);
     if (c <= 16384) return norm_shape<1024, 2>(a, stream);
     if (c <= 32768) return norm_shape<1024, 4>(a, stream);
     return norm_shape<1024, 8>(a, stream);

@@ -10,81 +10,124 @@ namespace {
 
 using namespace dev;
 
-// A workgroup takes rows blockIdx.x, + gridDim.x, ...; its lanes
-// keep the same columns for every row, so dw's sum over those rows stays in
-// registers and leaves once, as one fp32 partial row.
-template <int T, int P, int DB, int HB, int RB>
-__global__ __launch_bounds__(T) void rmsnorm_backward_kernel(const NormBackwardArgs a) {
-    __shared__ float part[2][T / 64];
-    const int t = threadIdx.x;
-    float dw[P][8];
-    float w[P][8];
+// Eight columns of one row, as loaded.
+template <int DB, int HB, int RB>
+struct Pack {
+    Raw8<DB> d;
+    Raw8<HB> h;
+    Raw8<RB == 0 ? 2 : RB> r;
+    __device__ __forceinline__ void load(const NormBackwardArgs& a, int64_t row, int c) {
+        d = load8<DB>(a.dy, row * a.ld_dy + c, a.cols - c);
+        h = load8<HB>(a.h, row * a.ld_h + c, a.cols - c);
+        if constexpr (RB != 0) r = load8<RB>(a.dres, row * a.ld_dr + c, a.cols - c);
+    }
+    // dot += g . xhat
+    __device__ __forceinline__ void reduce(const NormBackwardArgs& a, const float (&w)[8],
+                                           float rstd, float& dot) const {
+        float dy[8], x[8];
+        widen8<DB>(d, a.dy_dtype == ZERO_BF16, dy);
+        widen8<HB>(h, a.h_dtype == ZERO_BF16, x);
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-        const int c = (i * T + t) * 8;
-        if (a.w_dtype == ZERO_F32) {
-            const Raw8<4> r = load8<4>(a.weight, c, a.cols - c);
-            widen8<4>(r, false, w[i]);
-        } else {
-            const Raw8<2> r = load8<2>(a.weight, c, a.cols - c);
-            widen8<2>(r, a.w_dtype == ZERO_BF16, w[i]);
+        for (int k = 0; k < 8; ++k) dot = __builtin_fmaf(dy[k] * w[k], x[k] * rstd, dot);
+    }
+    __device__ __forceinline__ void finish(const NormBackwardArgs& a, int64_t row, int c,
+                                           const float (&w)[8], float rstd, float mean,
+                                           float (&dw)[8]) const {
+        float dy[8], x[8], dr[8];
+        widen8<DB>(d, a.dy_dtype == ZERO_BF16, dy);
+        widen8<HB>(h, a.h_dtype == ZERO_BF16, x);
+        if constexpr (RB != 0) widen8<RB>(r, a.dr_dtype == ZERO_BF16, dr);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const float xhat = x[k] * rstd;
+            dw[k] = __builtin_fmaf(dy[k], xhat, dw[k]);
+            const float inner = __builtin_fmaf(-xhat, mean, dy[k] * w[k]);
+            if constexpr (RB != 0) dy[k] = __builtin_fmaf(rstd, inner, dr[k]);
+            else dy[k] = rstd * inner;
         }
+        store8(a.dx, row * a.ld_dx + c, a.cols - c, a.dx_dtype, dy);
+    }
+};
+
+__device__ __forceinline__ void load_weight(const NormBackwardArgs& a, int c, float (&w)[8]) {
+    if (a.w_dtype == ZERO_F32) widen8<4>(load8<4>(a.weight, c, a.cols - c), false, w);
+    else widen8<2>(load8<2>(a.weight, c, a.cols - c), a.w_dtype == ZERO_BF16, w);
+}
+
+// A workgroup takes rows blockIdx.x, + gridDim.x, ...  Its lanes keep the same
+// columns for every row, so dw's sum over those rows stays in registers and
+// leaves once, as one fp32 partial row.  Up to 16,384 columns a row is held in
+// registers, and up to 8,192 the next one's loads are under way meanwhile; wider
+// rows are read again behind the reduction.
+template <int MAX_T, int P, int DB, int HB, int RB>
+__global__ __launch_bounds__(MAX_T) void rmsnorm_backward_kernel(const NormBackwardArgs a) {
+    __shared__ float part[2][16];
+    constexpr bool kHeld = P <= 2, kAhead = kHeld && MAX_T <= 512;
+    const int T = static_cast<int>(blockDim.x);
+    const int first = static_cast<int>(threadIdx.x) * 8;
+    const float inv_cols = 1.0f / static_cast<float>(a.cols);
+    float dw[P][8] = {}, w[kHeld ? P : 1][8];
+    Pack<DB, HB, RB> next[kAhead ? P : 1];
+    float next_rstd = 0.0f;
+    if constexpr (kAhead) {
+        next_rstd = a.rstd[blockIdx.x];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) dw[i][k] = 0.0f;
+        for (int i = 0; i < P; ++i) next[i].load(a, blockIdx.x, first + i * T * 8);
+    }
+    if constexpr (kHeld) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) load_weight(a, first + i * T * 8, w[i]);
     }
     int flip = 0;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, flip ^= 1) {
-        Raw8<DB> rd[P];
-        Raw8<HB> rh[P];
-        Raw8<RB == 0 ? 2 : RB> rr[P];
-        const float rstd = a.rstd[row];
-#pragma unroll
-        for (int i = 0; i < P; ++i) {
-            const int c = (i * T + t) * 8;
-            rd[i] = load8<DB>(a.dy, row * a.ld_dy + c, a.cols - c);
-            rh[i] = load8<HB>(a.h, row * a.ld_h + c, a.cols - c);
-            if constexpr (RB != 0) rr[i] = load8<RB>(a.dres, row * a.ld_dr + c, a.cols - c);
-        }
         float dot = 0.0f;
+        if constexpr (kHeld) {
+            Pack<DB, HB, RB> now[P];
+            float rstd;
+            if constexpr (kAhead) {
+                rstd = next_rstd;
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-            float d[8], h[8];
-            widen8<DB>(rd[i], a.dy_dtype == ZERO_BF16, d);
-            widen8<HB>(rh[i], a.h_dtype == ZERO_BF16, h);
-            const int left = a.cols - (i * T + t) * 8;
+                for (int i = 0; i < P; ++i) now[i] = next[i];
+                if (row + gridDim.x < a.rows) {
+                    next_rstd = a.rstd[row + gridDim.x];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const float xhat = h[k] * rstd;
-                // lanes behind the row's end hold zeros, which a non-finite
-                // rstd would make NaN
-                if (k < left) {
-                    dot = __builtin_fmaf(d[k] * w[i][k], xhat, dot);
-                    dw[i][k] = __builtin_fmaf(d[k], xhat, dw[i][k]);
+                    for (int i = 0; i < P; ++i) next[i].load(a, row + gridDim.x, first + i * T * 8);
                 }
-            }
-        }
-        const float mean = block_sum<T>(dot, part[flip]) / static_cast<float>(a.cols);
+            } else {
+                rstd = a.rstd[row];
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-            const int c = (i * T + t) * 8;
-            float d[8], h[8], r[8];
-            widen8<DB>(rd[i], a.dy_dtype == ZERO_BF16, d);
-            widen8<HB>(rh[i], a.h_dtype == ZERO_BF16, h);
-            if constexpr (RB != 0) widen8<RB>(rr[i], a.dr_dtype == ZERO_BF16, r);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const float xhat = h[k] * rstd;
-                const float inner = __builtin_fmaf(-xhat, mean, d[k] * w[i][k]);
-                if constexpr (RB != 0) d[k] = __builtin_fmaf(rstd, inner, r[k]);
-                else d[k] = rstd * inner;
+                for (int i = 0; i < P; ++i) now[i].load(a, row, first + i * T * 8);
             }
-            store8(a.dx, row * a.ld_dx + c, a.cols - c, a.dx_dtype, d);
+#pragma unroll
+            for (int i = 0; i < P; ++i) now[i].reduce(a, w[i], rstd, dot);
+            const float mean = block_sum(dot, part[flip]) * inv_cols;
+#pragma unroll
+            for (int i = 0; i < P; ++i)
+                now[i].finish(a, row, first + i * T * 8, w[i], rstd, mean, dw[i]);
+        } else {
+            const float rstd = a.rstd[row];
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                Pack<DB, HB, RB> now;
+                now.load(a, row, first + i * T * 8);
+                load_weight(a, first + i * T * 8, w[0]);
+                now.reduce(a, w[0], rstd, dot);
+            }
+            const float mean = block_sum(dot, part[flip]) * inv_cols;
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                Pack<DB, HB, RB> now;
+                now.load(a, row, first + i * T * 8);
+                load_weight(a, first + i * T * 8, w[0]);
+                now.finish(a, row, first + i * T * 8, w[0], rstd, mean, dw[i]);
+                __builtin_amdgcn_sched_barrier(0);  // one pack's registers at a time
+            }
         }
     }
     if (!a.parts) return;
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-        const int c = (i * T + t) * 8;
+        const int c = first + i * T * 8;
         store8(a.parts, static_cast<int64_t>(blockIdx.x) * a.cols + c, a.cols - c, ZERO_F32,
                dw[i]);
     }
@@ -94,7 +137,7 @@ __global__ __launch_bounds__(T) void rmsnorm_backward_kernel(const NormBackwardA
 // over the partial rows, then over the groups, in a fixed order.
 constexpr int kDwCols = 64;
 constexpr int kDwGroups = 16;
-__global__ __launch_bounds__(kDwCols* kDwGroups) void rmsnorm_dw_kernel(const float* parts,
+__global__ __launch_bounds__(kDwCols * kDwGroups) void rmsnorm_dw_kernel(const float* parts,
                                                                        int n_parts, int cols,
                                                                        void* dw, int dtype) {
     __shared__ float sums[kDwGroups][kDwCols];
@@ -122,31 +165,38 @@ __global__ __launch_bounds__(kDwCols* kDwGroups) void rmsnorm_dw_kernel(const fl
     }
 }
 
-template <int T, int P, int DB, int HB>
-void backward_types(const NormBackwardArgs& a, dim3 grid, hipStream_t stream) {
-    if (!a.dres) rmsnorm_backward_kernel<T, P, DB, HB, 0><<<grid, T, 0, stream>>>(a);
+template <int MAX_T, int P, int DB, int HB>
+void backward_types(const NormBackwardArgs& a, dim3 grid, dim3 block, hipStream_t stream) {
+    if (!a.dres) rmsnorm_backward_kernel<MAX_T, P, DB, HB, 0><<<grid, block, 0, stream>>>(a);
     else if (a.dr_dtype == ZERO_F32)
-        rmsnorm_backward_kernel<T, P, DB, HB, 4><<<grid, T, 0, stream>>>(a);
-    else rmsnorm_backward_kernel<T, P, DB, HB, 2><<<grid, T, 0, stream>>>(a);
+        rmsnorm_backward_kernel<MAX_T, P, DB, HB, 4><<<grid, block, 0, stream>>>(a);
+    else rmsnorm_backward_kernel<MAX_T, P, DB, HB, 2><<<grid, block, 0, stream>>>(a);
 }
 
-template <int T, int P>
+template <int MAX_T, int P>
 void backward_shape(const NormBackwardArgs& a, dim3 grid, hipStream_t stream) {
+    const dim3 block(static_cast<uint32_t>((a.cols + P * 512 - 1) / (P * 512) * 64));
     const bool d4 = a.dy_dtype == ZERO_F32, h4 = a.h_dtype == ZERO_F32;
     if (d4) {
-        if (h4) backward_types<T, P, 4, 4>(a, grid, stream);
-        else backward_types<T, P, 4, 2>(a, grid, stream);
+        if (h4) backward_types<MAX_T, P, 4, 4>(a, grid, block, stream);
+        else backward_types<MAX_T, P, 4, 2>(a, grid, block, stream);
     } else {
-        if (h4) backward_types<T, P, 2, 4>(a, grid, stream);
-        else backward_types<T, P, 2, 2>(a, grid, stream);
+        if (h4) backward_types<MAX_T, P, 2, 4>(a, grid, block, stream);
+        else backward_types<MAX_T, P, 2, 2>(a, grid, block, stream);
     }
 }
 
 }  // namespace
 
+// One workgroup per CU: beyond that dw's partial rows cost more than the extra
+// rows in flight bring.  8192 x 4096 (fp16 dy and dx, fp32 h): 68.2 us with 256,
+// 69.1 with 512, 71.3 with 768, 77.1 with 1,024; 1003 x 5001 in bf16: 21.8, 25.0,
+// 27.8 and 31.7.
 int32_t norm_backward_parts(int64_t rows, int32_t cols) {
     (void)cols;
-    return static_cast<int32_t>(rows < ZERO_NORM_MAX_PARTS ? rows : ZERO_NORM_MAX_PARTS);
+    constexpr int64_t kMost = 256;
+    static_assert(kMost <= ZERO_NORM_MAX_PARTS, "the documented limit");
+    return static_cast<int32_t>(rows < kMost ? rows : kMost);
 }
 
 hipError_t launch_rmsnorm_backward(const NormBackwardArgs& a, hipStream_t stream) {
@@ -155,9 +205,6 @@ hipError_t launch_rmsnorm_backward(const NormBackwardArgs& a, hipStream_t stream
     if (parts > 0) {
         const dim3 grid(static_cast<uint32_t>(parts));
         if (c <= 512) backward_shape<64, 1>(a, grid, stream);
-        else if (c <= 1024) backward_shape<64, 2>(a, grid, stream);
-        else if (c <= 2048) backward_shape<128, 2>(a, grid, stream);
-        else if (c <= 4096) backward_shape<256, 2>(a, grid, stream);
         else if (c <= 8192) backward_shape<512, 2>(a, grid, stream);
         else if (c <= 16384) backward_shape<1024, 2>(a, grid, stream);
         else if (c <= 32768) backward_shape<1024, 4>(a, grid, stream);
