@@ -139,7 +139,7 @@ __device__ __forceinline__ void store8(void* p, int64_t i, int n, int dtype, con
 // ---- 8-bit blocks --------------------------------------------------------
 
 struct BlockScale {
-    float inv;     // 2^-e
+    float scale;   // 2^e
     uint32_t byte; // e + 127, or 255
 };
 
@@ -154,53 +154,85 @@ __device__ __forceinline__ BlockScale block_scale(uint32_t amax_bits, int fmt) {
     e = e < -127 ? -127 : e;
     if (amax_bits == 0) e = 0;
     BlockScale r;
-    r.inv = as_float(static_cast<uint32_t>(127 - e) << 23);
-    r.byte = amax_bits >= 0x7f800000u ? 255u : static_cast<uint32_t>(e + 127);
+    r.byte = static_cast<uint32_t>(e + 127);
+    r.scale = as_float(r.byte == 0 ? 0x400000u : r.byte << 23);
+    if (amax_bits >= 0x7f800000u) r.byte = 255u;
     return r;
 }
 
-// Four scaled values as 8-bit floats, rounded to nearest even.
-__device__ __forceinline__ uint32_t pack4(float a, float b, float c, float d, int fmt) {
-    int r;
-    if (fmt == ZERO_E4M3) {
-        r = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
-        r = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, r, true);
+typedef short v2s __attribute__((ext_vector_type(2)));
+typedef _Float16 v2h __attribute__((ext_vector_type(2)));
+typedef __bf16 v2b __attribute__((ext_vector_type(2)));
+
+// Four values over 2^e as 8-bit floats, rounded to nearest even: one
+// instruction a pair divides, rounds and packs.
+template <int FMT>
+__device__ __forceinline__ uint32_t pack4(float a, float b, float c, float d, float scale) {
+    v2s r = {0, 0};
+    if constexpr (FMT == ZERO_E4M3) {
+        r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, a, b, scale, false);
+        r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, c, d, scale, true);
     } else {
-        r = __builtin_amdgcn_cvt_pk_bf8_f32(a, b, 0, false);
-        r = __builtin_amdgcn_cvt_pk_bf8_f32(c, d, r, true);
+        r = __builtin_amdgcn_cvt_scalef32_pk_bf8_f32(r, a, b, scale, false);
+        r = __builtin_amdgcn_cvt_scalef32_pk_bf8_f32(r, c, d, scale, true);
     }
-    return static_cast<uint32_t>(r);
+    return __builtin_bit_cast(uint32_t, r);
 }
+
+// The same of two words of two 16-bit values each.
+template <int FMT, bool BF16>
+__device__ __forceinline__ uint32_t pack4(uint32_t ab, uint32_t cd, float scale) {
+    v2s r = {0, 0};
+    if constexpr (BF16) {
+        const v2b x = __builtin_bit_cast(v2b, ab), y = __builtin_bit_cast(v2b, cd);
+        if constexpr (FMT == ZERO_E4M3) {
+            r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, x, scale, false);
+            r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, y, scale, true);
+        } else {
+            r = __builtin_amdgcn_cvt_scalef32_pk_bf8_bf16(r, x, scale, false);
+            r = __builtin_amdgcn_cvt_scalef32_pk_bf8_bf16(r, y, scale, true);
+        }
+    } else {
+        const v2h x = __builtin_bit_cast(v2h, ab), y = __builtin_bit_cast(v2h, cd);
+        if constexpr (FMT == ZERO_E4M3) {
+            r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f16(r, x, scale, false);
+            r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f16(r, y, scale, true);
+        } else {
+            r = __builtin_amdgcn_cvt_scalef32_pk_bf8_f16(r, x, scale, false);
+            r = __builtin_amdgcn_cvt_scalef32_pk_bf8_f16(r, y, scale, true);
+        }
+    }
+    return __builtin_bit_cast(uint32_t, r);
+}
+
+constexpr uint32_t kNan4 = 0x7f7f7f7fu;  // four NaNs in both types
 
 __device__ __forceinline__ u32x2 pack8(const float (&f)[8], const BlockScale& s, int fmt) {
-    if (s.byte == 255u) return u32x2{0x7f7f7f7fu, 0x7f7f7f7fu};  // NaN in both types
-    u32x2 r;
-    r[0] = pack4(f[0] * s.inv, f[1] * s.inv, f[2] * s.inv, f[3] * s.inv, fmt);
-    r[1] = pack4(f[4] * s.inv, f[5] * s.inv, f[6] * s.inv, f[7] * s.inv, fmt);
-    return r;
+    if (s.byte == 255u) return u32x2{kNan4, kNan4};
+    if (fmt == ZERO_E4M3)
+        return u32x2{pack4<ZERO_E4M3>(f[0], f[1], f[2], f[3], s.scale),
+                     pack4<ZERO_E4M3>(f[4], f[5], f[6], f[7], s.scale)};
+    return u32x2{pack4<ZERO_E5M2>(f[0], f[1], f[2], f[3], s.scale),
+                 pack4<ZERO_E5M2>(f[4], f[5], f[6], f[7], s.scale)};
 }
 
-__device__ __forceinline__ uint32_t abs_bits(float v) {
-    return as_bits(v) & 0x7fffffffu;
-}
+__device__ __forceinline__ uint32_t abs_bits(float v) { return as_bits(v) & 0x7fffffffu; }
+
+__device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
 
 __device__ __forceinline__ uint32_t amax8(const float (&f)[8]) {
     uint32_t m = 0;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        const uint32_t b = abs_bits(f[k]);
-        m = b > m ? b : m;
-    }
+    for (int k = 0; k < 8; ++k) m = umax(m, abs_bits(f[k]));
     return m;
 }
 
+// The largest of 16 neighbouring lanes', by rotations of the 16.
 __device__ __forceinline__ uint32_t max16lanes(uint32_t m) {
-#pragma unroll
-    for (int d = 1; d < 16; d *= 2) {
-        const uint32_t o = static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), d));
-        m = o > m ? o : m;
-    }
-    return m;
+    m = umax(m, __builtin_amdgcn_mov_dpp(static_cast<int>(m), 0x121, 0xf, 0xf, true));
+    m = umax(m, __builtin_amdgcn_mov_dpp(static_cast<int>(m), 0x122, 0xf, 0xf, true));
+    m = umax(m, __builtin_amdgcn_mov_dpp(static_cast<int>(m), 0x124, 0xf, 0xf, true));
+    return umax(m, __builtin_amdgcn_mov_dpp(static_cast<int>(m), 0x128, 0xf, 0xf, true));
 }
 
 // ---- reductions ----------------------------------------------------------

@@ -57,12 +57,13 @@ __device__ __forceinline__ void load_weight(const NormBackwardArgs& a, int c, fl
 // A workgroup takes rows blockIdx.x, + gridDim.x, ...  Its lanes keep the same
 // columns for every row, so dw's sum over those rows stays in registers and
 // leaves once, as one fp32 partial row.  Up to 16,384 columns a row is held in
-// registers, and up to 8,192 the next one's loads are under way meanwhile; wider
-// rows are read again behind the reduction.
+// registers, and up to 8,192 the next one's loads are under way meanwhile (one
+// pack per lane: more waves for the arithmetic of the one row, 1003 x 5001 17 us
+// against 20 with two packs); wider rows are read again behind the reduction.
 template <int MAX_T, int P, int DB, int HB, int RB>
 __global__ __launch_bounds__(MAX_T) void rmsnorm_backward_kernel(const NormBackwardArgs a) {
     __shared__ float part[2][16];
-    constexpr bool kHeld = P <= 2, kAhead = kHeld && MAX_T <= 512;
+    constexpr bool kHeld = P <= 2, kAhead = P == 1;
     const int T = static_cast<int>(blockDim.x);
     const int first = static_cast<int>(threadIdx.x) * 8;
     const float inv_cols = 1.0f / static_cast<float>(a.cols);
@@ -189,9 +190,9 @@ void backward_shape(const NormBackwardArgs& a, dim3 grid, hipStream_t stream) {
 }  // namespace
 
 // One workgroup per CU: beyond that dw's partial rows cost more than the extra
-// rows in flight bring.  8192 x 4096 (fp16 dy and dx, fp32 h): 68.2 us with 256,
-// 69.1 with 512, 71.3 with 768, 77.1 with 1,024; 1003 x 5001 in bf16: 21.8, 25.0,
-// 27.8 and 31.7.
+// rows in flight bring.  8192 x 4096 (fp16 dy and dx, fp32 h): 65.7 us with 256,
+// 5.1 TB/s, 69.2 with 512; 1003 x 5001 in bf16: 19.7 and 21.8, of which 5 are its
+// rows' odd addresses.
 int32_t norm_backward_parts(int64_t rows, int32_t cols) {
     (void)cols;
     constexpr int64_t kMost = 256;
@@ -205,7 +206,7 @@ hipError_t launch_rmsnorm_backward(const NormBackwardArgs& a, hipStream_t stream
     if (parts > 0) {
         const dim3 grid(static_cast<uint32_t>(parts));
         if (c <= 512) backward_shape<64, 1>(a, grid, stream);
-        else if (c <= 8192) backward_shape<512, 2>(a, grid, stream);
+        else if (c <= 8192) backward_shape<1024, 1>(a, grid, stream);
         else if (c <= 16384) backward_shape<1024, 2>(a, grid, stream);
         else if (c <= 32768) backward_shape<1024, 4>(a, grid, stream);
         else backward_shape<1024, 8>(a, grid, stream);
