@@ -205,8 +205,8 @@ int zero_rmsnorm_backward(const void* dy, int32_t dy_dtype, int64_t ld_dy, const
  * with w = row_weight[r] (the caller's mask and mean) and S the loss scale.  An
  * index that comes twice counts twice.  An entry with p_j = 0 (a logit of
  * -inf) adds nothing, whatever q is there.
- *   - A row of weight 0 gives loss 0, lse 0 and gradient 0; its logits and
- *     entries are not read, so they may hold anything.
+ *   - A row of weight 0 gives loss 0, lse 0 and gradient 0, whatever its
+ *     logits and entries hold.
  *   - A row with no entry left (all negative indices, or logits of -inf) gives
  *     loss 0 and gradient 0.
  *   - A row with an index >= vocab, a NaN or +inf among its entries, a NaN or

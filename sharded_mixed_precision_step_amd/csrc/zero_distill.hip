@@ -2,12 +2,20 @@
 //
 // One workgroup per row.  The student's row goes by once for the running
 // maximum and sum of its softmax (fp32, from a finite start so that a row of
-// -inf stays countable) and once more for the gradient.  The teacher's entries,
-// at most 1,024, sit in LDS.  The gradient is first written as coef * q_v for
-// the whole row; behind a barrier the entries' places are written again with
-// their p_j taken off, each computed from the logit read before anything was
-// written, so that one rounding is made and the gradient may take the
-// logits' place.
+// -inf stays countable) and once more for the gradient.  Rows of up to 32,768
+// elements stay in registers in between; longer ones are read twice, the second
+// time mostly from the memory-side cache, which the gradient's streaming stores
+// leave to them: 4096 x 131072 fp16 takes 429 us, 5.0 TB/s over the logits read
+// once and the gradient written once (494 us with ordinary stores, 524 us also
+// with half the loads under way; 751 us with the row held in 64 registers a lane,
+// where loading, summing and writing do not overlap).
+//
+// The teacher's entries lie one to four per lane; their softmax joins across
+// the workgroup together with the row's, behind one barrier.  The gradient is
+// first written as coef * q_v for the whole row; behind a second barrier the
+// entries' places are written again with their p_j taken off, each computed
+// from the logit read before anything was written, so that one rounding is
+// made and the gradient may take the logits' place.
 #include "zero_device.h"
 #include "zero_train_internal.h"
 
@@ -18,12 +26,13 @@ using namespace dev;
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLowest = -3.402823466e38f;
+constexpr int kUnroll = 4;  // packs of eight a lane has under way
 
-// exp(x) for x * log2(e) formed by the caller
+// 2^x by the hardware's instruction: one step off at most
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
 struct Stat {
-    float m, s;  // running maximum, sum of exp2((x - m) * c)
+    float m, s;  // running maximum, sum of 2^((x - m) c)
 };
 
 __device__ __forceinline__ Stat join(Stat a, Stat b, float c) {
@@ -31,43 +40,117 @@ __device__ __forceinline__ Stat join(Stat a, Stat b, float c) {
     return {m, a.s * exp2_fast((a.m - m) * c) + b.s * exp2_fast((b.m - m) * c)};
 }
 
-// One teacher entry per thread and step; T threads.
-constexpr int kT = 1024;
-
-struct Entries {
-    int32_t idx[ZERO_DISTILL_MAX_TOP];
-    float p[ZERO_DISTILL_MAX_TOP];
-    float x[ZERO_DISTILL_MAX_TOP];  // the student's logit there, times 1
-    float red[2 * (kT / 64)];
-    int32_t bad;
-};
-
-__device__ __forceinline__ float block_max(float v, float* part) {
-    v = wave_max(v);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
-    __syncthreads();
-    float s = part[0];
+// Over each N neighbouring lanes; the same bits on all of them.
+template <int N>
+__device__ __forceinline__ Stat lanes_join(Stat st, float c) {
 #pragma unroll
-    for (int w = 1; w < kT / 64; ++w) s = fmaxf(s, part[w]);
-    return s;
+    for (int d = 1; d < N; d *= 2)
+        st = join(st, {__shfl_xor(st.m, d), __shfl_xor(st.s, d)}, c);
+    return st;
 }
 
-__device__ __forceinline__ float block_add(float v, float* part) {
-    __syncthreads();
-    return block_sum(v, part);
+// Pack `at` bytes behind a row's body: the body in scalar registers, so that a
+// lane's packs share one offset.
+typedef __amdgpu_buffer_rsrc_t Buffer;
+template <int B>
+__device__ __forceinline__ Raw8<B> load_pack(Buffer body, int lane, int at) {
+    Raw8<B> r;
+#pragma unroll
+    for (int k = 0; k < B / 2; ++k)
+        r.v[k] = __builtin_bit_cast(
+            u32x4, __builtin_amdgcn_raw_buffer_load_b128(body, lane, at + 16 * k, 0));
+    return r;
 }
 
-template <int B, DistillMode MODE>
-__global__ __launch_bounds__(kT) void distill_kernel(const DistillArgs a) {
-    __shared__ Entries e;
-    const int t = threadIdx.x;
+template <int B>
+__device__ __forceinline__ Raw8<B> load_aligned(const char* at) {
+    Raw8<B> r;
+#pragma unroll
+    for (int k = 0; k < B / 2; ++k) r.v[k] = reinterpret_cast<const u32x4*>(at)[k];
+    return r;
+}
+
+// N packs into a running statistic: one maximum and one rescaling for them all.
+template <int B, int N>
+__device__ __forceinline__ void take(Stat& st, const Raw8<B> (&r)[N], bool bf16, float c) {
+    float f[N][8];
+    float m = st.m;
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+        widen8<B>(r[u], bf16, f[u]);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) m = fmaxf(m, f[u][k]);
+    }
+    st.s *= exp2_fast((st.m - m) * c);
+    st.m = m;
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+        float s = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) s += exp2_fast((f[u][k] - m) * c);
+        st.s += s;
+    }
+}
+
+// T lanes per row; R > 0: the row's body is at most R * T packs, and stays in
+// registers.
+template <int DT, int T, int R, DistillMode MODE>
+__global__ __launch_bounds__(T, 4) void distill_kernel(const DistillArgs a) {
+    constexpr int B = DT == ZERO_F32 ? 4 : 2;
+    constexpr bool bf16 = DT == ZERO_BF16, kHeld = R > 0;
+    constexpr int kWaves = T / 64, kEntries = ZERO_DISTILL_MAX_TOP / T;
+    __shared__ __attribute__((aligned(16))) int32_t entry_index[ZERO_DISTILL_MAX_TOP];
+    __shared__ __attribute__((aligned(16))) float entry_p[ZERO_DISTILL_MAX_TOP];
+    __shared__ Stat row_part[kWaves], top_part[kWaves];
+    __shared__ float loss_part[kWaves];
+    __shared__ int32_t bad_part[kWaves];
+    const int t = threadIdx.x, wave = t / 64;
     const int64_t row = blockIdx.x;
-    const bool bf16 = a.dtype == ZERO_BF16;
     const float weight = a.weight ? a.weight[row] : 1.0f;
     const int vocab = static_cast<int>(a.vocab);
     const char* x = static_cast<const char*>(a.logits) + row * a.ld * B;
     char* g = static_cast<char*>(a.grad) + row * a.ld_grad * B;
+    // The row as a head up to the first 16-byte border, packs of eight, and a
+    // tail; head and tail, at most 14 elements, lie one to a lane.
+    int head = static_cast<int>(-reinterpret_cast<uintptr_t>(x) & 15) / B;
+    head = head < vocab ? head : vocab;
+    const int packs = (vocab - head) / 8, tail = head + 8 * packs;
+    const int edge = t < head ? t : t - head < vocab - tail ? tail + t - head : -1;
+    // what is known where to find goes first, all of it at once
+    int64_t given[kEntries];
+    float top[kEntries];
+#pragma unroll
+    for (int k = 0; k < kEntries; ++k) {
+        given[k] = -1;
+        top[k] = 0.0f;
+        if (t + k * T < a.top) {
+            const int64_t at = row * a.ld_top + t + k * T;
+            given[k] = a.index_bytes == 8 ? static_cast<const int64_t*>(a.index)[at]
+                                          : static_cast<const int32_t*>(a.index)[at];
+            top[k] = load1(a.top_logit, at, a.top_dtype);
+        }
+    }
+    const char* body = x + head * B;
+    const float edge_x = edge >= 0 ? load1(x, edge, DT) : -__builtin_inff();
+
+    Raw8<B> held[kHeld ? R : 1];
+    if constexpr (kHeld) {
+        // places behind the row read as -inf
+        constexpr uint32_t kInf32 = 0xff800000u;
+        const uint32_t fill = B == 4 ? kInf32 : bf16 ? 0xff80ff80u : 0xfc00fc00u;
+        const Buffer buffer =
+            __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(body), 0, -1, 0x00020000);
+#pragma unroll
+        for (int u = 0; u < R; ++u) {
+            if ((u + 1) * T <= packs || t + u * T < packs) {
+                held[u] = load_pack<B>(buffer, t * 8 * B, u * T * 8 * B);
+            } else {
+#pragma unroll
+                for (int k = 0; k < B / 2; ++k) held[u].v[k] = u32x4{fill, fill, fill, fill};
+            }
+        }
+    }
+
     if (weight == 0.0f) {
         if (MODE != kDistillBackward && t == 0) {
             if (a.loss) a.loss[row] = 0.0f;
@@ -75,143 +158,218 @@ __global__ __launch_bounds__(kT) void distill_kernel(const DistillArgs a) {
         }
         if (MODE != kDistillForward) {
             const float zero[8] = {};
-            for (int v = 8 * t; v < vocab; v += 8 * kT) store8(g, v, vocab - v, a.dtype, zero);
+            for (int64_t v = 8 * t; v < vocab; v += 8 * T)
+                store8(g, v, static_cast<int>(vocab - v), DT, zero);
         }
         return;
     }
-    if (t == 0) e.bad = 0;
-    __syncthreads();
-    // entries, at most one per thread
-    const float inv_tau = 1.0f / a.tau;
-    float tl = kLowest;
-    bool have = false;
-    int32_t idx = -1;
-    if (t < a.top) {
-        const int64_t at = row * a.ld_top + t;
-        const int64_t i = a.index_bytes == 8 ? static_cast<const int64_t*>(a.index)[at]
-                                             : static_cast<const int32_t*>(a.index)[at];
-        if (i >= vocab) {
-            e.bad = 1;
-        } else if (i >= 0) {
-            const float v = load1(a.top_logit, at, a.top_dtype);
-            if (!(v < __builtin_inff())) {
-                e.bad = 1;  // NaN or +inf
-            } else if (v > -__builtin_inff()) {
-                have = true;
-                tl = v / a.tau;
-            }
-            idx = static_cast<int32_t>(i);
-        }
-        e.idx[t] = idx;
-        e.x[t] = idx >= 0 ? load1(x, idx, a.dtype) : 0.0f;
-    }
-    const float tmax = block_max(tl, e.red);
-    const float pe = have ? expf(tl - tmax) : 0.0f;
-    const float psum = block_add(pe, e.red);
-    const float p = have ? pe / psum : 0.0f;
-    if (t < a.top) e.p[t] = p;
-    const bool empty = psum == 0.0f;
 
-    const float c = kLog2e * inv_tau;
-    float lse, m = 0.0f, log2s = 0.0f;
-    if (MODE != kDistillBackward) {
-        Stat st = {kLowest, 0.0f};
-        for (int v = 8 * t; v < vocab; v += 8 * kT) {
-            const Raw8<B> r = load8<B>(x, v, vocab - v);
-            float f[8];
-            widen8<B>(r, bf16, f);
-            if (v + 8 > vocab) {
+    // the teacher's entries
+    const float inv_tau = 1.0f / a.tau, c = kLog2e * inv_tau;
+    int32_t index[kEntries];
+    float at_index[kEntries];
+    bool have[kEntries], bad = false;
+    Stat top_stat = {kLowest, 0.0f};
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (v + k >= vocab) f[k] = -__builtin_inff();
+    for (int k = 0; k < kEntries; ++k) {
+        index[k] = -1;
+        at_index[k] = 0.0f;
+        have[k] = false;
+        const float v = top[k];
+        top[k] = kLowest;
+        if (given[k] >= vocab) {
+            bad = true;
+        } else if (given[k] >= 0) {
+            index[k] = static_cast<int32_t>(given[k]);
+            at_index[k] = load1(x, given[k], DT);
+            if (!(v < __builtin_inff())) bad = true;  // NaN or +inf
+            else if (v > -__builtin_inff()) {
+                have[k] = true;
+                top[k] = v / a.tau;
             }
-            float pm = st.m;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) pm = fmaxf(pm, f[k]);
-            st.s *= exp2_fast((st.m - pm) * c);
-            st.m = pm;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) st.s += exp2_fast((f[k] - pm) * c);
         }
+        if (have[k]) top_stat = join(top_stat, {top[k], 1.0f}, kLog2e);
+    }
+
+    // the row's statistic
+    Stat st = {kLowest, 0.0f};
+    if constexpr (MODE != kDistillBackward) {
+        if constexpr (kHeld) {
+            // one at a time: its fp32 values have to fit beside the row
 #pragma unroll
-        for (int d = 1; d < 64; d *= 2) {
-            const Stat o = {__shfl_xor(st.m, d), __shfl_xor(st.s, d)};
-            st = join(st, o, c);
-        }
-        __syncthreads();
-        if ((t & 63) == 0) {
-            e.red[t >> 6] = st.m;
-            e.red[kT / 64 + (t >> 6)] = st.s;
-        }
-        __syncthreads();
-        st = {e.red[0], e.red[kT / 64]};
+            for (int u = 0; u < R; ++u) {
+                const Raw8<B> r[1] = {held[u]};
+                take(st, r, bf16, c);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        } else {
+            int p0 = 0;
+            for (; p0 + kUnroll * T <= packs; p0 += kUnroll * T) {
+                Raw8<B> r[kUnroll];
 #pragma unroll
-        for (int w = 1; w < kT / 64; ++w) st = join(st, {e.red[w], e.red[kT / 64 + w]}, c);
+                for (int u = 0; u < kUnroll; ++u)
+                    r[u] = load_aligned<B>(body + static_cast<int64_t>(p0 + u * T + t) * 8 * B);
+                take(st, r, bf16, c);
+            }
+            for (int p = p0 + t; p < packs; p += T) {
+                const Raw8<B> r[1] = {load_aligned<B>(body + static_cast<int64_t>(p) * 8 * B)};
+                take(st, r, bf16, c);
+            }
+        }
+        if (edge >= 0) {
+            const float m = fmaxf(st.m, edge_x);
+            st.s = st.s * exp2_fast((st.m - m) * c) + exp2_fast((edge_x - m) * c);
+            st.m = m;
+        }
+        st = lanes_join<64>(st, c);
+    }
+    top_stat = lanes_join<64>(top_stat, kLog2e);
+    const bool wave_bad = __ballot(bad) != 0;
+    if ((t & 63) == 0) {
+        if (MODE != kDistillBackward) row_part[wave] = st;
+        top_part[wave] = top_stat;
+        bad_part[wave] = wave_bad;
+    }
+    __syncthreads();
+    // every wave joins the waves' parts, one to a lane
+    const int part = t % kWaves;
+    if (MODE != kDistillBackward) st = lanes_join<kWaves>(row_part[part], c);
+    top_stat = lanes_join<kWaves>(top_part[part], kLog2e);
+    bad = __ballot(bad_part[part]) != 0;
+
+    const bool empty = top_stat.s == 0.0f;
+    const float inv_top = 1.0f / top_stat.s, log_top = logf(top_stat.s);
+    float m = 0.0f, log2s = 0.0f, lse;
+    if constexpr (MODE == kDistillBackward) {
+        lse = bad ? __builtin_nanf("") : a.lse_in[row];
+    } else {
         m = st.m;
         log2s = log2f(st.s);
-        lse = st.s > 0.0f ? m * inv_tau + logf(st.s) : __builtin_nanf("");
-        if (e.bad) lse = __builtin_nanf("");
-        // the loss, one entry per thread
+        const float log_s = logf(st.s);
+        lse = st.s > 0.0f && !bad ? m * inv_tau + log_s : __builtin_nanf("");
         float term = 0.0f;
-        if (have && p > 0.0f) term = p * ((tl - tmax - logf(psum)) - (e.x[t] * inv_tau - lse));
-        const float kl = block_add(term, e.red);
-        if (t == 0) {
-            if (a.lse) a.lse[row] = lse;
-            if (a.loss)
-                a.loss[row] = lse != lse ? lse : empty ? 0.0f : weight * a.tau * a.tau * kl;
+#pragma unroll
+        for (int k = 0; k < kEntries; ++k) {
+            if (!have[k]) continue;
+            const float p = exp2_fast((top[k] - top_stat.m) * kLog2e) * inv_top;
+            const float log_p = top[k] - top_stat.m - log_top;
+            const float log_q = (at_index[k] - m) * inv_tau - log_s;
+            if (p > 0.0f) term += p * (log_p - log_q);
         }
-    } else {
-        lse = a.lse_in[row];
-        if (e.bad) lse = __builtin_nanf("");
+        term = wave_sum(term);
+        if ((t & 63) == 0) loss_part[wave] = term;
     }
-    if (MODE == kDistillForward) return;
 
-    const float S = a.ctl ? a.ctl->scale : a.S;
-    float coef = S * weight * a.tau;
-    if (empty) coef = 0.0f;
+    float coef = 0.0f;
     // q_v from the maximum and the sum, or from lse alone: the difference
     // first, so that large logits do not overflow on their way
     auto prob = [&](float v) {
-        if (MODE == kDistillBackward)
-            return exp2_fast(__builtin_fmaf(v, inv_tau, -lse) * kLog2e);
+        if (MODE == kDistillBackward) return exp2_fast(__builtin_fmaf(v, inv_tau, -lse) * kLog2e);
         return exp2_fast(__builtin_fmaf(v - m, c, -log2s));
     };
-    if (lse != lse) coef = lse;
-    __syncthreads();
-    for (int v = 8 * t; v < vocab; v += 8 * kT) {
-        const Raw8<B> r = load8<B>(x, v, vocab - v);
-        float f[8];
-        widen8<B>(r, bf16, f);
+    if constexpr (MODE != kDistillForward) {
+        coef = (a.ctl ? a.ctl->scale : a.S) * weight * a.tau;
+        if (empty) coef = 0.0f;
+        if (lse != lse) coef = lse;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const float q = prob(f[k]);
-            f[k] = empty && coef == 0.0f ? 0.0f : coef * q;
+        for (int k = 0; k < kEntries; ++k) {
+            const int j = t + k * T;
+            entry_index[j] = index[k];
+            entry_p[j] = have[k] ? exp2_fast((top[k] - top_stat.m) * kLog2e) * inv_top : 0.0f;
         }
-        store8(g, v, vocab - v, a.dtype, f);
+        char* g_body = g + head * B;
+        auto put = [&](const Raw8<B>& r, int p) {
+            float f[8];
+            widen8<B>(r, bf16, f);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) f[k] = coef * prob(f[k]);
+            store8<true>(g_body, static_cast<int64_t>(p) * 8, 8, DT, f);
+        };
+        if (empty && coef == 0.0f) {
+            const float zero[8] = {};
+            for (int64_t v = 8 * t; v < vocab; v += 8 * T)
+                store8(g, v, static_cast<int>(vocab - v), DT, zero);
+        } else {
+            if constexpr (kHeld) {
+#pragma unroll
+                for (int u = 0; u < R; ++u) {
+                    if ((u + 1) * T <= packs || t + u * T < packs) put(held[u], t + u * T);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            } else {
+                int p0 = 0;
+                for (; p0 + kUnroll * T <= packs; p0 += kUnroll * T) {
+                    Raw8<B> r[kUnroll];
+#pragma unroll
+                    for (int u = 0; u < kUnroll; ++u)
+                        r[u] = load_aligned<B>(body + static_cast<int64_t>(p0 + u * T + t) * 8 * B);
+#pragma unroll
+                    for (int u = 0; u < kUnroll; ++u) put(r[u], p0 + u * T + t);
+                }
+                for (int p = p0 + t; p < packs; p += T)
+                    put(load_aligned<B>(body + static_cast<int64_t>(p) * 8 * B), p);
+            }
+            if (edge >= 0) store1(g, edge, DT, coef * prob(edge_x));
+        }
     }
     __syncthreads();
-    if (t < a.top && idx >= 0 && !empty) {
-        float taken = 0.0f;
-        for (int j = 0; j < a.top; ++j)
-            if (e.idx[j] == idx) taken += e.p[j];
-        const float q = prob(e.x[t]);
-        store1(g, idx, a.dtype, coef * (q - taken));
+    if (MODE != kDistillBackward && t == 0) {
+        float kl = loss_part[0];
+        for (int w = 1; w < kWaves; ++w) kl += loss_part[w];
+        if (a.lse) a.lse[row] = lse;
+        if (a.loss) a.loss[row] = lse != lse ? lse : empty ? 0.0f : weight * a.tau * a.tau * kl;
+    }
+    if constexpr (MODE != kDistillForward) {
+        if (empty) return;
+        const int groups = (a.top + 3) / 4;  // behind a.top: index -1
+#pragma unroll
+        for (int k = 0; k < kEntries; ++k) {
+            if (index[k] < 0) continue;
+            float taken = 0.0f;
+            for (int j = 0; j < groups; ++j) {
+                const int4 i4 = reinterpret_cast<const int4*>(entry_index)[j];
+                const float4 p4 = reinterpret_cast<const float4*>(entry_p)[j];
+                taken += i4.x == index[k] ? p4.x : 0.0f;
+                taken += i4.y == index[k] ? p4.y : 0.0f;
+                taken += i4.z == index[k] ? p4.z : 0.0f;
+                taken += i4.w == index[k] ? p4.w : 0.0f;
+            }
+            store1(g, index[k], DT, coef * (prob(at_index[k]) - taken));
+        }
+    }
+}
+
+template <int DT, DistillMode MODE>
+void distill_size(const DistillArgs& a, hipStream_t stream) {
+    const dim3 grid(static_cast<uint32_t>(a.rows));
+    // Lanes per row: 256 where they hold it (37 rows of 32,001: 9.1 us held by 1,024,
+    // 14.7 us in two passes).  Two passes in one call: 1,024 lanes, so that fewer
+    // rows wait in the cache (4096 x 131072: 433 us, 489 with 512); one pass: 512
+    // (2048 x 50001, both calls: 134 us, 174 with 1,024, before streaming stores).
+    if (a.vocab <= 256 * kUnroll * 8) {
+        distill_kernel<DT, 256, kUnroll, MODE><<<grid, 256, 0, stream>>>(a);
+    } else if constexpr (MODE == kDistillBoth) {
+        if (a.vocab <= 1024 * kUnroll * 8)
+            distill_kernel<DT, 1024, kUnroll, MODE><<<grid, 1024, 0, stream>>>(a);
+        else distill_kernel<DT, 1024, 0, MODE><<<grid, 1024, 0, stream>>>(a);
+    } else {
+        distill_kernel<DT, 512, 0, MODE><<<grid, 512, 0, stream>>>(a);
     }
 }
 
 template <DistillMode MODE>
-void distill_mode(const DistillArgs& a, hipStream_t stream) {
-    const dim3 grid(static_cast<uint32_t>(a.rows));
-    if (a.dtype == ZERO_F32) distill_kernel<4, MODE><<<grid, kT, 0, stream>>>(a);
-    else distill_kernel<2, MODE><<<grid, kT, 0, stream>>>(a);
+void distill_type(const DistillArgs& a, hipStream_t stream) {
+    if (a.dtype == ZERO_F32) distill_size<ZERO_F32, MODE>(a, stream);
+    else if (a.dtype == ZERO_F16) distill_size<ZERO_F16, MODE>(a, stream);
+    else distill_size<ZERO_BF16, MODE>(a, stream);
 }
 
 }  // namespace
 
 hipError_t launch_distill(const DistillArgs& a, DistillMode mode, hipStream_t stream) {
-    if (mode == kDistillForward) distill_mode<kDistillForward>(a, stream);
-    else if (mode == kDistillBackward) distill_mode<kDistillBackward>(a, stream);
-    else distill_mode<kDistillBoth>(a, stream);
+    if (mode == kDistillForward) distill_type<kDistillForward>(a, stream);
+    else if (mode == kDistillBackward) distill_type<kDistillBackward>(a, stream);
+    else distill_type<kDistillBoth>(a, stream);
     return hipGetLastError();
 }
 
