@@ -127,7 +127,7 @@ int quantize(const void* const* srcs, int n_srcs, int32_t dtype, int64_t rows, i
         n_out += 2;
     }
     if ((rc = check_apart(out, n_out, in, n_srcs, who))) return rc;
-    if (zero::quantize_blocks(rows, cols) > kMaxGrid || cols > (int64_t{1} << 37))
+    if (zero::quantize_blocks(rows, cols) > kMaxGrid)
         return fail(ZERO_EINVAL, "%s: the matrix is larger than one launch covers", who);
     zero::QuantizeArgs a = {};
     a.src[0] = srcs[0];
@@ -281,7 +281,8 @@ int zero_q8_gemm(const void* a, int32_t fmt_a, int64_t ld_a, const uint8_t* sa, 
     if (accumulate != 0 && accumulate != 1)
         return fail(ZERO_EINVAL, "%s: accumulate = %d is neither 0 nor 1", who, accumulate);
     if (m == 0 || n == 0) return ok();
-    if (k > ZERO_Q8_MAX_LD || ld_a > ZERO_Q8_MAX_LD || ld_b > ZERO_Q8_MAX_LD)
+    if (k > ZERO_Q8_MAX_LD || ld_a > ZERO_Q8_MAX_LD || ld_b > ZERO_Q8_MAX_LD ||
+        ld_sa > ZERO_Q8_MAX_LD || ld_sb > ZERO_Q8_MAX_LD)
         return fail(ZERO_ERANGE, "%s: k or a row stride is above %d", who, ZERO_Q8_MAX_LD);
     Array ins[4], out;
     if ((rc = check_q8(a, ld_a, sa, ld_sa, m, k, who, "a", "sa", &ins[0], &ins[1])) ||
