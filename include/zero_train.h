@@ -43,9 +43,9 @@
  * power of two that brings the block's largest magnitude to the type's largest
  * value or below, so that nothing saturates and scaling is exact; e is held
  * to [-127, 127]; a block of zeros has scale 1.  A block with an inf or a NaN
- * has scale byte 255 (NaN) and NaN elements, so that every product it enters
- * is NaN and the overflow check of the step sees it.  Power-of-two scales are
- * what gfx950's matrix cores apply themselves.
+ * has scale byte 255 (NaN) and NaN elements, padding included, so that every
+ * product it enters is NaN and the overflow check of the step sees it.
+ * Power-of-two scales are what gfx950's matrix cores apply themselves.
  */
 #ifndef ZERO_TRAIN_H
 #define ZERO_TRAIN_H
@@ -118,7 +118,8 @@ int zero_q8_quantize_ctl(const void* const* srcs_fp16, int64_t rows, int64_t col
  * y = x w^T (a = x, b = w), dx = dy w (a = dy, b = w transposed) and
  * dw = dy^T x (a = dy transposed, b = x transposed).  k == 0 gives zeros.
  * c must not overlap a, b or their scales.  Returns ZERO_OK, ZERO_EINVAL,
- * ZERO_EALIGN, ZERO_ERANGE (k or a row stride above ZERO_Q8_MAX_LD) or ZERO_EHIP.
+ * ZERO_EALIGN, ZERO_ERANGE (k or a row stride above ZERO_Q8_MAX_LD) or ZERO_EHIP;
+ * ZERO_EINVAL also for a c of more than 2^27 tiles of 64 x 64.
  */
 int zero_q8_gemm(const void* a, int32_t fmt_a, int64_t ld_a, const uint8_t* sa, int64_t ld_sa,
                  const void* b, int32_t fmt_b, int64_t ld_b, const uint8_t* sb, int64_t ld_sb,
@@ -145,8 +146,10 @@ int zero_q8_gemm(const void* a, int32_t fmt_a, int64_t ld_a, const uint8_t* sa, 
  *   rstd                       fp32[rows], or NULL
  * At least one of h, y, q and rstd is given.  Apart from the cases named, no
  * output may overlap an input or another output.  A row with a non-finite h
- * gives NaN, or inf, where the formula does.  rows == 0 is a no-op.  Returns
- * ZERO_OK, ZERO_EINVAL, ZERO_EALIGN, ZERO_ERANGE (cols) or ZERO_EHIP.
+ * gives NaN, or inf, where the formula does; sums of squares are fp32's, so
+ * that rows beyond 1.8e19, which no fp16 row is, count as infinitely long.
+ * rows == 0 is a no-op.  Returns ZERO_OK, ZERO_EINVAL, ZERO_EALIGN, ZERO_ERANGE
+ * (cols) or ZERO_EHIP.
  */
 int zero_rmsnorm(const void* x, int32_t x_dtype, int64_t ld_x, const void* residual,
                  int32_t r_dtype, int64_t ld_r, const void* weight, int32_t w_dtype, int64_t rows,
@@ -227,7 +230,7 @@ typedef struct zero_distill_inputs {
     int32_t top_dtype;       /* of top_logit                                     */
     int32_t index_bytes;     /* 4 or 8                                           */
     int32_t top;             /* entries per row, 1 .. ZERO_DISTILL_MAX_TOP       */
-    float temperature;       /* finite, > 0                                      */
+    float temperature;       /* > 0; it, its square and log2(e) / it finite      */
     int32_t pad_;
 } zero_distill_inputs;
 
@@ -241,9 +244,9 @@ typedef struct zero_distill_inputs {
  * be given here, for instance the weight times a gradient that arrives at each
  * row's loss (for a row whose lse was taken with weight 0, only 0).  q_v is
  * taken from lse, which fp32 holds to 2^-24 of its size: logits / temperature of
- * magnitude Z put an error of Z * 2^-23 on q_v (zero_distill has none of it).
- * grad may be
- * the logits themselves (same ld).  S is loss_scale, or, when d_ctl is not NULL,
+ * magnitude Z put an error of Z * 2^-23 on q_v, and a row whose logits /
+ * temperature all lie beyond fp32 has no such lse (zero_distill has none of
+ * this).  grad may be the logits themselves (same ld).  S is loss_scale, or, when d_ctl is not NULL,
  * d_ctl->scale, the scale of the control block's next step, read on the
  * device; loss_scale is then not used.
  *

@@ -164,7 +164,8 @@ __global__ __launch_bounds__(T, 4) void distill_kernel(const DistillArgs a) {
         return;
     }
 
-    // the teacher's entries
+    // the teacher's entries; divided by the temperature as differences only, so
+    // that logits of the type's lowest value stay in range
     const float inv_tau = 1.0f / a.tau, c = kLog2e * inv_tau;
     int32_t index[kEntries];
     float at_index[kEntries];
@@ -185,10 +186,10 @@ __global__ __launch_bounds__(T, 4) void distill_kernel(const DistillArgs a) {
             if (!(v < __builtin_inff())) bad = true;  // NaN or +inf
             else if (v > -__builtin_inff()) {
                 have[k] = true;
-                top[k] = v / a.tau;
+                top[k] = v;
             }
         }
-        if (have[k]) top_stat = join(top_stat, {top[k], 1.0f}, kLog2e);
+        if (have[k]) top_stat = join(top_stat, {top[k], 1.0f}, c);
     }
 
     // the row's statistic
@@ -223,7 +224,7 @@ __global__ __launch_bounds__(T, 4) void distill_kernel(const DistillArgs a) {
         }
         st = lanes_join<64>(st, c);
     }
-    top_stat = lanes_join<64>(top_stat, kLog2e);
+    top_stat = lanes_join<64>(top_stat, c);
     const bool wave_bad = __ballot(bad) != 0;
     if ((t & 63) == 0) {
         if (MODE != kDistillBackward) row_part[wave] = st;
@@ -234,7 +235,7 @@ __global__ __launch_bounds__(T, 4) void distill_kernel(const DistillArgs a) {
     // every wave joins the waves' parts, one to a lane
     const int part = t % kWaves;
     if (MODE != kDistillBackward) st = lanes_join<kWaves>(row_part[part], c);
-    top_stat = lanes_join<kWaves>(top_part[part], kLog2e);
+    top_stat = lanes_join<kWaves>(top_part[part], c);
     bad = __ballot(bad_part[part]) != 0;
 
     const bool empty = top_stat.s == 0.0f;
@@ -251,8 +252,8 @@ __global__ __launch_bounds__(T, 4) void distill_kernel(const DistillArgs a) {
 #pragma unroll
         for (int k = 0; k < kEntries; ++k) {
             if (!have[k]) continue;
-            const float p = exp2_fast((top[k] - top_stat.m) * kLog2e) * inv_top;
-            const float log_p = top[k] - top_stat.m - log_top;
+            const float p = exp2_fast((top[k] - top_stat.m) * c) * inv_top;
+            const float log_p = (top[k] - top_stat.m) * inv_tau - log_top;
             const float log_q = (at_index[k] - m) * inv_tau - log_s;
             if (p > 0.0f) term += p * (log_p - log_q);
         }
@@ -275,7 +276,7 @@ __global__ __launch_bounds__(T, 4) void distill_kernel(const DistillArgs a) {
         for (int k = 0; k < kEntries; ++k) {
             const int j = t + k * T;
             entry_index[j] = index[k];
-            entry_p[j] = have[k] ? exp2_fast((top[k] - top_stat.m) * kLog2e) * inv_top : 0.0f;
+            entry_p[j] = have[k] ? exp2_fast((top[k] - top_stat.m) * c) * inv_top : 0.0f;
         }
         char* g_body = g + head * B;
         auto put = [&](const Raw8<B>& r, int p) {

@@ -2,10 +2,14 @@
 //
 // One workgroup takes a 128 x 128 tile: the unit in which a block along a row
 // and a block along a column are both whole, so one pass over src serves both
-// outputs.  Bound by HBM.  By rows a block of 128 lies in 16 lanes' registers
-// and its scale is found by shuffles.  For the transposed output the tile
-// turns in LDS: it is written as loaded, read down its columns, and the 8-bit
-// result is turned once more so that stores run along qt's rows.
+// outputs.  By rows a block of 128 lies in 16 lanes' registers and its scale is
+// found by lane rotations.  For the transposed output the tile turns in LDS: it
+// is written as loaded, read down its columns, and the 8-bit result is turned
+// once more so that stores run along qt's rows.
+//
+// Bound by HBM: 14336 x 4096 fp16 in both forms takes 50 us, 4.7 TB/s, as a large
+// copy (69 us with scaling and conversion as instructions of their own); by
+// rows alone 36, transposed alone 38.
 #include "zero_device.h"
 #include "zero_train_internal.h"
 

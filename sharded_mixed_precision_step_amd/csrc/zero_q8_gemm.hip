@@ -558,12 +558,7 @@ Variant choose(int64_t m, int64_t n, int64_t steps) {
 
 }  // namespace
 
-int64_t gemm_blocks(int64_t m, int64_t n, int32_t kblocks) {
-    const Variant v = choose(m, n, kblocks);
-    if (v == kRowsKernel) return (n + 15) / 16;
-    const int64_t side = v == kLarge ? 256 : v == kSmall ? 64 : 128;
-    return (m + side - 1) / side * ((n + side - 1) / side);
-}
+int64_t gemm_tiles(int64_t m, int64_t n) { return (m + 63) / 64 * ((n + 63) / 64); }
 
 hipError_t launch_q8_gemm(const GemmArgs& a, hipStream_t stream) {
     switch (choose(a.m, a.n, a.kblocks)) {

@@ -15,6 +15,7 @@ using zero::ok;
 using zero::overlap;
 
 constexpr int64_t kMaxGrid = 0x7fffffff;   // workgroups of one launch
+constexpr int64_t kMaxTiles = int64_t{1} << 27;  // a band of eight rows of them fits 32 bits
 constexpr int64_t kMaxBytes = int64_t{1} << 56;
 
 // A strided array of one call: what overlap checks and messages need.
@@ -165,10 +166,10 @@ int distill(const zero_distill_inputs* in, zero::DistillMode mode, float loss_sc
     if (in->top > ZERO_DISTILL_MAX_TOP)
         return fail(ZERO_ERANGE, "%s: top = %d is above %d", who, in->top, ZERO_DISTILL_MAX_TOP);
     if (!finite_f(in->temperature) || !(in->temperature > 0.0f) ||
-        !finite_f(1.0f / in->temperature) ||
+        !finite_f(1.442695041f / in->temperature) ||
         !finite_f(in->temperature * in->temperature))
         return fail(ZERO_EINVAL, "%s: temperature = %g is not finite and > 0, or its square or "
-                    "reciprocal is not finite", who, static_cast<double>(in->temperature));
+                    "log2(e) by it is not finite", who, static_cast<double>(in->temperature));
     if (mode != zero::kDistillForward) {
         if (ctl) {
             if ((rc = check_ctl(ctl, who))) return rc;
@@ -298,7 +299,7 @@ int zero_q8_gemm(const void* a, int32_t fmt_a, int64_t ld_a, const uint8_t* sa, 
     g.kblocks = static_cast<int32_t>((k + 127) / 128);
     g.fmt_a = fmt_a; g.fmt_b = fmt_b; g.c_dtype = c_dtype; g.accumulate = accumulate;
     g.c = c; g.ld_c = ld_c;
-    if (zero::gemm_blocks(m, n, g.kblocks) > kMaxGrid)
+    if (zero::gemm_tiles(m, n) > kMaxTiles)
         return fail(ZERO_EINVAL, "%s: c is larger than one launch covers", who);
     const hipError_t e = zero::launch_q8_gemm(g, static_cast<hipStream_t>(stream));
     return e == hipSuccess ? ok() : hip_fail(e, who);

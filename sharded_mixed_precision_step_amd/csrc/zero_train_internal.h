@@ -30,7 +30,7 @@ struct GemmArgs {
     void* c;
     int64_t ld_c;
 };
-int64_t gemm_blocks(int64_t m, int64_t n, int32_t kblocks);
+int64_t gemm_tiles(int64_t m, int64_t n);
 hipError_t launch_q8_gemm(const GemmArgs& a, hipStream_t stream);
 
 struct NormArgs {

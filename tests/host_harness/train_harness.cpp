@@ -75,7 +75,7 @@ int hip_fail(hipError_t, const char* where) { return fail(ZERO_EHIP, "%s", where
 int64_t quantize_blocks(int64_t rows, int64_t cols) {
     return (rows + 127) / 128 * ((cols + 127) / 128);
 }
-int64_t gemm_blocks(int64_t m, int64_t n, int32_t) { return (m + 63) / 64 * ((n + 63) / 64); }
+int64_t gemm_tiles(int64_t m, int64_t n) { return (m + 63) / 64 * ((n + 63) / 64); }
 int32_t norm_backward_parts(int64_t rows, int32_t) {
     return static_cast<int32_t>(rows < 256 ? rows : 256);
 }

@@ -245,3 +245,24 @@ def test_distill_past_2_31_elements():
     assert float(loss.min()) == float(loss.max())
     assert (grad[:, :top] == 1024.0 * (1 / vocab - 0.25)).all()
     assert (grad[-1, top:] == 1024.0 / vocab).all() and (grad[:, top:] == 1024.0 / vocab).all()
+
+
+@pytest.mark.parametrize("two", [False, True])
+@pytest.mark.parametrize("tdtype", [F32, BF16, F16])
+@pytest.mark.parametrize("tau", [0.25, 3.0])
+def test_distill_teacher_logits_of_the_lowest_value(tau, tdtype, two):
+    """Masks of the type's lowest value: beside others, no mass, as -inf (fp16's
+    lowest is 65504 / 3 below anything here, of no mass in fp32 either); a row
+    of nothing else is uniform, as any row of equal logits.  Divided by a
+    temperature below 1 they leave fp32's range."""
+    device()
+    logits, index, teacher, weight = _case(6, 700, 9, F16, tdtype)
+    lowest = torch.finfo(tdtype).min
+    teacher[1], teacher[2, ::2], teacher[3, 1:] = lowest, lowest, lowest
+    teacher[4] = torch.finfo(tdtype).max
+    same = teacher.clone()
+    same[1], same[2, ::2], same[3, 1:], same[4] = 0, -math.inf, -math.inf, 0
+    got = _run(logits, index, teacher, tau, weight, 64.0, two)
+    want = _run(logits, index, same, tau, weight, 64.0, two)
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+    _check(logits, index, same, tau, weight, 64.0, two)

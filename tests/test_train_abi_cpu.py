@@ -124,6 +124,14 @@ def test_gemm_refuses(kw, code, word):
     _refused(_gemm(**kw), code, word)
 
 
+def test_gemm_refuses_more_tiles_than_it_numbers():
+    """2^27 tiles of 64 x 64; no columns of k, so that c alone is large."""
+    wide = dict(k=0, m=1, a=None, sa=None, b=None, sb=None)
+    _refused(_gemm(**wide, n=(64 << 27) + 1, ldc=1 << 34), EINVAL, "launch")
+    _refused(_gemm(**wide, n=1 << 54, ldc=1 << 54), EINVAL, "launch")
+    _refused(_gemm(**dict(wide, m=(64 << 26) + 1, n=65, ldc=65)), EINVAL, "launch")
+
+
 def _norm(**kw):
     a = dict(x=A, xt=1, ldx=200, res=B, rt=0, ldr=200, w=C, wt=1, rows=4, cols=200, eps=1e-5, h=D,
              ldh=200, y=E, yt=1, ldy=200, q=F, fmt=0, ldq=256, s=G, lds=4, rstd=8 * P)
@@ -211,6 +219,12 @@ NAMES = ["zero_distill_forward", "zero_distill_backward", "zero_distill"]
 ])
 def test_distill_refuses(name, kw, code, word):
     _refused(_distill(name, **kw), code, word)
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_distill_refuses_a_temperature_too_small_to_divide_by(name):
+    """1 / 3.5e-39 is in fp32's range, log2(e) / 3.5e-39 is not."""
+    _refused(_distill(name, tau=3.5e-39), EINVAL, "temperature")
 
 
 @pytest.mark.parametrize("name", NAMES[1:])
