@@ -163,10 +163,11 @@ constexpr int kXcds = 8, kBand = 8;
 struct Tile {
     int m, n;
 };
-__device__ __forceinline__ Tile tile_of(int block, int tiles_m, int tiles_n) {
-    const int total = tiles_m * tiles_n, each = total / kXcds, extra = total % kXcds;
-    const int xcd = block % kXcds;
-    const int p = xcd * each + (xcd < extra ? xcd : extra) + block / kXcds;
+__device__ __forceinline__ int place_of(int block, int total) {
+    const int each = total / kXcds, extra = total % kXcds, xcd = block % kXcds;
+    return xcd * each + (xcd < extra ? xcd : extra) + block / kXcds;
+}
+__device__ __forceinline__ Tile tile_of(int p, int tiles_m, int tiles_n) {
     const int band = p / (kBand * tiles_n), in = p - band * kBand * tiles_n;
     const int rows = tiles_m - band * kBand < kBand ? tiles_m - band * kBand : kBand;
     return {band * kBand + in % rows, in / rows};
@@ -329,20 +330,17 @@ __device__ __forceinline__ void step(const Loader<BM, BN, WAVES>& loader, int k,
     }
 }
 
-template <int BM, int BN, int WM, int WN, int STAGES, int FA, int FB>
-__global__ __launch_bounds__(64 * WM * WN, 2) void q8_gemm_kernel(const GemmArgs a, int tiles_m,
-                                                               int tiles_n) {
+// c's rows m0 .. m0 + BM - 1, columns n0 .. n0 + BN - 1.  Step k goes through
+// buffer k % STAGES, of 2 or 4 (lds2 is lds0 and lds3 lds1 if they are 2), of
+// BYTES each; `scales` holds four steps' bytes per row, a's rows first.
+template <int BM, int BN, int WM, int WN, int STAGES, int BYTES, int FA, int FB>
+__device__ __forceinline__ void gemm_tile(const GemmArgs& a, int64_t m0, int64_t n0, uint8_t* lds0,
+                                          uint8_t* lds1, uint8_t* lds2, uint8_t* lds3,
+                                          uint32_t* scales) {
+    static_assert(STAGES == 2 || STAGES == 4, "the loop takes four steps at a time");
     constexpr int kWaves = WM * WN;
     constexpr int MI = BM / WM / 32, NI = BN / WN / 32;
-    // STAGES buffers, step k in buffer k % STAGES; as arrays of their own (see step)
-    static_assert(STAGES == 2 || STAGES == 4, "the loop takes four steps at a time");
-    constexpr int kBytes = (BM + BN) * kStep;
-    __shared__ __attribute__((aligned(16))) uint8_t lds0[kBytes], lds1[kBytes];
-    __shared__ __attribute__((aligned(16))) uint8_t lds2_[STAGES == 4 ? kBytes : 16];
-    __shared__ __attribute__((aligned(16))) uint8_t lds3_[STAGES == 4 ? kBytes : 16];
-    uint8_t* const lds2 = STAGES == 4 ? lds2_ : lds0;
-    uint8_t* const lds3 = STAGES == 4 ? lds3_ : lds1;
-    __shared__ uint32_t scales[BM + BN];  // four steps' bytes per row, a's rows first
+    static_assert((BM + BN) * kStep <= BYTES, "a step has one buffer");
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), l = threadIdx.x % 64;
     const int row_a = wave / WN * (BM / WM), row_b = wave % WN * (BN / WN);
     const int at_a = fragment_offset(row_a), at_b = BM * kStep + fragment_offset(row_b);
@@ -353,11 +351,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void q8_gemm_kernel(const GemmArgs
     const int last = steps - 1;  // behind it the last step is loaded again, for nobody
     auto clamped = [&](int k) { return k < last ? k : last; };
     using Out = Turn<32 * NI>;
-    static_assert(Out::kBytes * kWaves <= kBytes, "the turn has one buffer");
+    static_assert(Out::kBytes * kWaves <= BYTES, "the turn has one buffer");
     uint8_t* const turn = lds1 + wave * Out::kBytes;
 
-    const Tile tile = tile_of(static_cast<int>(blockIdx.x), tiles_m, tiles_n);
-    const int64_t m0 = static_cast<int64_t>(tile.m) * BM, n0 = static_cast<int64_t>(tile.n) * BN;
     const Loader<BM, BN, kWaves> loader(a, m0, n0);
     v16f acc[MI][NI];
 #pragma unroll
@@ -413,6 +409,35 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void q8_gemm_kernel(const GemmArgs
         if (plain && a.c_dtype == ZERO_F16) put_rows<32 * NI, ZERO_F16>(a, row, col, turn);
         else if (plain) put_rows<32 * NI, ZERO_BF16>(a, row, col, turn);
         else put_any<32 * NI>(a, row, col, turn);
+    }
+}
+
+// Workgroups 0 .. whole - 1 take a tile each, the first `whole` of them; of the
+// others two share a tile, one the upper half of its rows and one the lower.
+template <int BM, int BN, int WM, int WN, int STAGES, bool HALVES, int FA, int FB>
+__global__ __launch_bounds__(64 * WM * WN, 2) void q8_gemm_kernel(const GemmArgs a, int tiles_m,
+                                                               int tiles_n, int whole) {
+    // the buffers are arrays of their own (see step)
+    constexpr int kBytes = (BM + BN) * kStep;
+    __shared__ __attribute__((aligned(16))) uint8_t lds0[kBytes], lds1[kBytes];
+    __shared__ __attribute__((aligned(16))) uint8_t lds2_[STAGES == 4 ? kBytes : 16];
+    __shared__ __attribute__((aligned(16))) uint8_t lds3_[STAGES == 4 ? kBytes : 16];
+    uint8_t* const lds2 = STAGES == 4 ? lds2_ : lds0;
+    uint8_t* const lds3 = STAGES == 4 ? lds3_ : lds1;
+    __shared__ uint32_t scales[BM + BN];
+    const int block = static_cast<int>(blockIdx.x);
+    if (!HALVES || block < whole) {
+        const Tile tile = tile_of(place_of(block, whole), tiles_m, tiles_n);
+        gemm_tile<BM, BN, WM, WN, STAGES, kBytes, FA, FB>(a, static_cast<int64_t>(tile.m) * BM,
+                                                          static_cast<int64_t>(tile.n) * BN, lds0,
+                                                          lds1, lds2, lds3, scales);
+    } else if constexpr (HALVES) {
+        const int p = place_of(block - whole, 2 * (tiles_m * tiles_n - whole));
+        const Tile tile = tile_of(whole + p / 2, tiles_m, tiles_n);
+        const int64_t m0 = static_cast<int64_t>(tile.m) * BM + p % 2 * (BM / 2);
+        if (m0 >= a.m) return;
+        gemm_tile<BM / 2, BN, WM, WN, STAGES, kBytes, FA, FB>(
+            a, m0, static_cast<int64_t>(tile.n) * BN, lds0, lds1, lds2, lds3, scales);
     }
 }
 
@@ -508,29 +533,37 @@ hipError_t gemm_rows(const GemmArgs& a, hipStream_t stream) {
     return hipGetLastError();
 }
 
-template <int BM, int BN, int WM, int WN, int STAGES>
+// Tiles of the large kernel that two workgroups share.  A CU holds one of its
+// workgroups, so that the tiles left over by the rounds of 256 would keep at most
+// half of the CUs busy if they are 128 or fewer.  14336 x 4096 x 2176 (896 tiles,
+// three rounds and a half): 114 to 122 us, 119 to 139 with whole tiles only;
+// 4352 x 8192 x 4096 (544 tiles) 135, 148.  Where no tile is shared the kernel
+// takes the same time with and without this.
+int64_t halved(int64_t tiles) { return tiles % 256 <= 128 ? tiles % 256 : 0; }
+
+template <int BM, int BN, int WM, int WN, int STAGES, bool HALVES = false>
 hipError_t gemm_formats(const GemmArgs& a, hipStream_t stream) {
     const int tm = static_cast<int>((a.m + BM - 1) / BM), tn = static_cast<int>((a.n + BN - 1) / BN);
-    const dim3 grid(static_cast<uint32_t>(static_cast<int64_t>(tm) * tn)), block(64 * WM * WN);
+    const int total = tm * tn, whole = HALVES ? total - halved(total) : total;
+    const dim3 grid(static_cast<uint32_t>(2 * total - whole)), block(64 * WM * WN);
+    auto run = [&](auto kernel) { kernel<<<grid, block, 0, stream>>>(a, tm, tn, whole); };
     if (a.fmt_a == ZERO_E4M3) {
-        if (a.fmt_b == ZERO_E4M3)
-            q8_gemm_kernel<BM, BN, WM, WN, STAGES, 0, 0><<<grid, block, 0, stream>>>(a, tm, tn);
-        else q8_gemm_kernel<BM, BN, WM, WN, STAGES, 0, 1><<<grid, block, 0, stream>>>(a, tm, tn);
+        if (a.fmt_b == ZERO_E4M3) run(q8_gemm_kernel<BM, BN, WM, WN, STAGES, HALVES, 0, 0>);
+        else run(q8_gemm_kernel<BM, BN, WM, WN, STAGES, HALVES, 0, 1>);
     } else {
-        if (a.fmt_b == ZERO_E4M3)
-            q8_gemm_kernel<BM, BN, WM, WN, STAGES, 1, 0><<<grid, block, 0, stream>>>(a, tm, tn);
-        else q8_gemm_kernel<BM, BN, WM, WN, STAGES, 1, 1><<<grid, block, 0, stream>>>(a, tm, tn);
+        if (a.fmt_b == ZERO_E4M3) run(q8_gemm_kernel<BM, BN, WM, WN, STAGES, HALVES, 1, 0>);
+        else run(q8_gemm_kernel<BM, BN, WM, WN, STAGES, HALVES, 1, 1>);
     }
     return hipGetLastError();
 }
 
 // Which kernel, by an estimate of its time in ns: rounds of tiles over the 256
-// CUs times steps of k, with the coefficients that fit the times of 420 sizes
-// (m 1 .. 8192, n 64 .. 14336, k 512 .. 4096); the choice is 0.2 % off the best
-// of the four in the mean and 9 % at worst.  At k = 4096, in us (256 x 256,
-// 128 x 128, 128 x 128 with eight waves, 64 x 64):
-//   8192 x 14336   385  470  656  734        2048 x 4096   46   36   44   57
-//   1024 x  4096    45   31   25   30         256 x 1024   39   19   21    8
+// CUs times steps of k, with the coefficients that fit the times of 360 sizes
+// (m 48 .. 8192, n 64 .. 14336, k 512 .. 4096); the choice is 0.4 % off the best
+// of the four in the mean and 20 % at worst (1500 x 14336 x 512, 26.8 us for 22.3).
+// At k = 4096, in us (256 x 256, 128 x 128, 128 x 128 with eight waves, 64 x 64):
+//   8192 x 14336   385  470  656  734        2048 x 4096   37   36   44   57
+//   1024 x  4096    32   29   24   29         256 x 1024   39   19   21    8
 // A single round takes what its longest chain of loads takes: the large tiles
 // have the least traffic per product, the small ones are done soonest.
 // Up to 16 rows and 4,096 columns: the rows kernel, 7.9 us at 16 x 4096 against
@@ -545,7 +578,9 @@ Variant choose(int64_t m, int64_t n, int64_t steps) {
         return (tiles(side) + at_once - 1) / at_once;
     };
     const int64_t behind = tiles(64) > 128 ? tiles(64) - 128 : 0;
-    const int64_t ns[4] = {rounds(256, 256) * (1480 * steps + 7700),
+    const int64_t large = tiles(256), shared = halved(large);
+    const int64_t ns[4] = {(large - shared + 255) / 256 * (1480 * steps + 7700) +
+                               (shared ? 1050 * steps + 4400 : 0),
                            rounds(128, 512) * (970 * steps + 2700),
                            rounds(128, 256) * (790 * steps + 3800),
                            220 * steps + 1900 + behind * (940 * steps + 2000) / 1000};
@@ -563,7 +598,7 @@ int64_t gemm_tiles(int64_t m, int64_t n) { return (m + 63) / 64 * ((n + 63) / 64
 hipError_t launch_q8_gemm(const GemmArgs& a, hipStream_t stream) {
     switch (choose(a.m, a.n, a.kblocks)) {
         case kRowsKernel: return gemm_rows(a, stream);
-        case kLarge: return gemm_formats<256, 256, 2, 4, 2>(a, stream);
+        case kLarge: return gemm_formats<256, 256, 2, 4, 2, true>(a, stream);
         case kMedium: return gemm_formats<128, 128, 2, 2, 2>(a, stream);
         case kMediumEight: return gemm_formats<128, 128, 2, 4, 4>(a, stream);
         case kSmall: break;
