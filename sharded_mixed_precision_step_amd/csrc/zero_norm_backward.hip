@@ -16,21 +16,24 @@ struct Pack {
     Raw8<DB> d;
     Raw8<HB> h;
     Raw8<RB == 0 ? 2 : RB> r;
-    __device__ __forceinline__ void load(const NormBackwardArgs& a, int64_t row, int c) {
-        d = load8<DB>(a.dy, row * a.ld_dy + c, a.cols - c);
-        h = load8<HB>(a.h, row * a.ld_h + c, a.cols - c);
-        if constexpr (RB != 0) r = load8<RB>(a.dres, row * a.ld_dr + c, a.cols - c);
+    __device__ __forceinline__ void load(const NormBackwardArgs& a, int64_t row, int c, int n) {
+        d = load8<DB>(a.dy, row * a.ld_dy + c, n);
+        h = load8<HB>(a.h, row * a.ld_h + c, n);
+        if constexpr (RB != 0) r = load8<RB>(a.dres, row * a.ld_dr + c, n);
     }
-    // dot += g . xhat
-    __device__ __forceinline__ void reduce(const NormBackwardArgs& a, const float (&w)[8],
+    // dot += g . xhat, of the elements from `from` on
+    __device__ __forceinline__ void reduce(const NormBackwardArgs& a, const float (&w)[8], int from,
                                            float rstd, float& dot) const {
         float dy[8], x[8];
         widen8<DB>(d, a.dy_dtype == ZERO_BF16, dy);
         widen8<HB>(h, a.h_dtype == ZERO_BF16, x);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) dot = __builtin_fmaf(dy[k] * w[k], x[k] * rstd, dot);
+        for (int k = 0; k < 8; ++k) {
+            const float sum = __builtin_fmaf(dy[k] * w[k], x[k] * rstd, dot);
+            dot = k >= from ? sum : dot;
+        }
     }
-    __device__ __forceinline__ void finish(const NormBackwardArgs& a, int64_t row, int c,
+    __device__ __forceinline__ void finish(const NormBackwardArgs& a, int64_t row, int c, int n,
                                            const float (&w)[8], float rstd, float mean,
                                            float (&dw)[8]) const {
         float dy[8], x[8], dr[8];
@@ -45,13 +48,14 @@ struct Pack {
             if constexpr (RB != 0) dy[k] = __builtin_fmaf(rstd, inner, dr[k]);
             else dy[k] = rstd * inner;
         }
-        store8(a.dx, row * a.ld_dx + c, a.cols - c, a.dx_dtype, dy);
+        store8(a.dx, row * a.ld_dx + c, n, a.dx_dtype, dy);
     }
 };
 
-__device__ __forceinline__ void load_weight(const NormBackwardArgs& a, int c, float (&w)[8]) {
-    if (a.w_dtype == ZERO_F32) widen8<4>(load8<4>(a.weight, c, a.cols - c), false, w);
-    else widen8<2>(load8<2>(a.weight, c, a.cols - c), a.w_dtype == ZERO_BF16, w);
+__device__ __forceinline__ void load_weight(const NormBackwardArgs& a, int c, int n,
+                                            float (&w)[8]) {
+    if (a.w_dtype == ZERO_F32) widen8<4>(load8<4>(a.weight, c, n), false, w);
+    else widen8<2>(load8<2>(a.weight, c, n), a.w_dtype == ZERO_BF16, w);
 }
 
 // A workgroup takes rows blockIdx.x, + gridDim.x, ...  Its lanes keep the same
@@ -60,24 +64,38 @@ __device__ __forceinline__ void load_weight(const NormBackwardArgs& a, int c, fl
 // registers, and up to 8,192 the next one's loads are under way meanwhile (one
 // pack per lane: more waves for the arithmetic of the one row, 1003 x 5001 17 us
 // against 20 with two packs); wider rows are read again behind the reduction.
+//
+// Where a row's length is no multiple of eight, a held row's last pack is its
+// last eight elements: what it shares with the pack before goes into the row's
+// sum once, and comes out of both alike.  (A tail loaded by elements stops its
+// wave until they are there, and the next row's loads with it: 8000 x 5001 in
+// bf16 117 us, 8000 x 5000 60.)  Rows read twice may not, since dx may be dy.
 template <int MAX_T, int P, int DB, int HB, int RB>
 __global__ __launch_bounds__(MAX_T) void rmsnorm_backward_kernel(const NormBackwardArgs a) {
     __shared__ float part[2][16];
     constexpr bool kHeld = P <= 2, kAhead = P == 1;
     const int T = static_cast<int>(blockDim.x);
-    const int first = static_cast<int>(threadIdx.x) * 8;
     const float inv_cols = 1.0f / static_cast<float>(a.cols);
+    // where pack i of the lane starts, its elements, and how many are another's
+    int at[P], n[P], from[P];
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+        const int c = (i * T + static_cast<int>(threadIdx.x)) * 8;
+        at[i] = kHeld && c > a.cols - 8 ? a.cols - 8 : c;
+        n[i] = kHeld ? 8 : a.cols - c;
+        from[i] = c - at[i];
+    }
     float dw[P][8] = {}, w[kHeld ? P : 1][8];
     Pack<DB, HB, RB> next[kAhead ? P : 1];
     float next_rstd = 0.0f;
     if constexpr (kAhead) {
         next_rstd = a.rstd[blockIdx.x];
 #pragma unroll
-        for (int i = 0; i < P; ++i) next[i].load(a, blockIdx.x, first + i * T * 8);
+        for (int i = 0; i < P; ++i) next[i].load(a, blockIdx.x, at[i], n[i]);
     }
     if constexpr (kHeld) {
 #pragma unroll
-        for (int i = 0; i < P; ++i) load_weight(a, first + i * T * 8, w[i]);
+        for (int i = 0; i < P; ++i) load_weight(a, at[i], n[i], w[i]);
     }
     int flip = 0;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, flip ^= 1) {
@@ -92,55 +110,56 @@ __global__ __launch_bounds__(MAX_T) void rmsnorm_backward_kernel(const NormBackw
                 if (row + gridDim.x < a.rows) {
                     next_rstd = a.rstd[row + gridDim.x];
 #pragma unroll
-                    for (int i = 0; i < P; ++i) next[i].load(a, row + gridDim.x, first + i * T * 8);
+                    for (int i = 0; i < P; ++i) next[i].load(a, row + gridDim.x, at[i], n[i]);
                 }
             } else {
                 rstd = a.rstd[row];
 #pragma unroll
-                for (int i = 0; i < P; ++i) now[i].load(a, row, first + i * T * 8);
+                for (int i = 0; i < P; ++i) now[i].load(a, row, at[i], n[i]);
             }
 #pragma unroll
-            for (int i = 0; i < P; ++i) now[i].reduce(a, w[i], rstd, dot);
+            for (int i = 0; i < P; ++i) now[i].reduce(a, w[i], from[i], rstd, dot);
             const float mean = block_sum(dot, part[flip]) * inv_cols;
 #pragma unroll
             for (int i = 0; i < P; ++i)
-                now[i].finish(a, row, first + i * T * 8, w[i], rstd, mean, dw[i]);
+                if (from[i] < 8) now[i].finish(a, row, at[i], n[i], w[i], rstd, mean, dw[i]);
         } else {
             const float rstd = a.rstd[row];
 #pragma unroll
             for (int i = 0; i < P; ++i) {
                 Pack<DB, HB, RB> now;
-                now.load(a, row, first + i * T * 8);
-                load_weight(a, first + i * T * 8, w[0]);
-                now.reduce(a, w[0], rstd, dot);
+                now.load(a, row, at[i], n[i]);
+                load_weight(a, at[i], n[i], w[0]);
+                now.reduce(a, w[0], 0, rstd, dot);
             }
             const float mean = block_sum(dot, part[flip]) * inv_cols;
 #pragma unroll
             for (int i = 0; i < P; ++i) {
                 Pack<DB, HB, RB> now;
-                now.load(a, row, first + i * T * 8);
-                load_weight(a, first + i * T * 8, w[0]);
-                now.finish(a, row, first + i * T * 8, w[0], rstd, mean, dw[i]);
+                now.load(a, row, at[i], n[i]);
+                load_weight(a, at[i], n[i], w[0]);
+                now.finish(a, row, at[i], n[i], w[0], rstd, mean, dw[i]);
                 __builtin_amdgcn_sched_barrier(0);  // one pack's registers at a time
             }
         }
     }
     if (!a.parts) return;
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-        const int c = first + i * T * 8;
-        store8(a.parts, static_cast<int64_t>(blockIdx.x) * a.cols + c, a.cols - c, ZERO_F32,
-               dw[i]);
-    }
+    for (int i = 0; i < P; ++i)
+        if (from[i] < 8)
+            store8(a.parts, static_cast<int64_t>(blockIdx.x) * a.cols + at[i], n[i], ZERO_F32,
+                   dw[i]);
 }
 
 // dw = the partial rows' sum: 64 columns per workgroup, 16 groups of lanes
-// over the partial rows, then over the groups, in a fixed order.
-constexpr int kDwCols = 64;
-constexpr int kDwGroups = 16;
-__global__ __launch_bounds__(kDwCols * kDwGroups) void rmsnorm_dw_kernel(const float* parts,
-                                                                       int n_parts, int cols,
-                                                                       void* dw, int dtype) {
+// over the partial rows, then over the groups, in a fixed order.  Up to 2,048
+// columns 32 and 32, so that there are workgroups enough (8192 x 1024, 1,024
+// partial rows: 4.8 us, 6.0 with 64 and 16; 5,001 columns, 256 rows: 4.9 and 4.4).
+constexpr int kDwThreads = 1024;
+template <int kDwCols>
+__global__ __launch_bounds__(kDwThreads) void rmsnorm_dw_kernel(const float* parts, int n_parts,
+                                                                int cols, void* dw, int dtype) {
+    constexpr int kDwGroups = kDwThreads / kDwCols;
     __shared__ float sums[kDwGroups][kDwCols];
     const int lane = threadIdx.x % kDwCols, group = threadIdx.x / kDwCols;
     const int c = blockIdx.x * kDwCols + lane;
@@ -189,15 +208,20 @@ void backward_shape(const NormBackwardArgs& a, dim3 grid, hipStream_t stream) {
 
 }  // namespace
 
-// One workgroup per CU: beyond that dw's partial rows cost more than the extra
-// rows in flight bring.  8192 x 4096 (fp16 dy and dx, fp32 h): 65.7 us with 256,
-// 5.1 TB/s, 69.2 with 512; 1003 x 5001 in bf16: 19.7 and 21.8, of which 5 are its
-// rows' odd addresses.
+// Workgroups, each with a partial row of dw.  One per CU beyond 2,048 columns:
+// more rows at a time bring less than their partial rows cost (8192 x 4096, fp16
+// dy and dx, fp32 h: 65 us with 256, 5.1 TB/s, 69 with 512).  Narrower rows are
+// few waves each and need more of them to fill the CUs, four rows each at least
+// (bf16, 8192 x 1024: 20 us with 1,024, 36 with 256; 1003 x 1024: 9 with 256, 12
+// with 1,003).
+//
+// 1003 x 5001 in bf16: 15.1 us, of which the sum of the partial rows is 4.4; rows
+// at odd addresses cost little there, a fifth at 8000 rows (80 us, 70).
 int32_t norm_backward_parts(int64_t rows, int32_t cols) {
-    (void)cols;
-    constexpr int64_t kMost = 256;
-    static_assert(kMost <= ZERO_NORM_MAX_PARTS, "the documented limit");
-    return static_cast<int32_t>(rows < kMost ? rows : kMost);
+    int64_t parts = cols <= 1024 ? 1024 : cols <= 2048 ? 512 : 256;
+    static_assert(ZERO_NORM_MAX_PARTS >= 1024, "the documented limit");
+    while (parts > 256 && rows < 4 * parts) parts /= 2;
+    return static_cast<int32_t>(rows < parts ? rows : parts);
 }
 
 hipError_t launch_rmsnorm_backward(const NormBackwardArgs& a, hipStream_t stream) {
@@ -205,7 +229,8 @@ hipError_t launch_rmsnorm_backward(const NormBackwardArgs& a, hipStream_t stream
     const int parts = norm_backward_parts(a.rows, c);
     if (parts > 0) {
         const dim3 grid(static_cast<uint32_t>(parts));
-        if (c <= 512) backward_shape<64, 1>(a, grid, stream);
+        if (c < 8) backward_shape<1024, 4>(a, grid, stream);  // no eight elements: by elements
+        else if (c <= 512) backward_shape<64, 1>(a, grid, stream);
         else if (c <= 8192) backward_shape<1024, 1>(a, grid, stream);
         else if (c <= 16384) backward_shape<1024, 2>(a, grid, stream);
         else if (c <= 32768) backward_shape<1024, 4>(a, grid, stream);
@@ -214,9 +239,12 @@ hipError_t launch_rmsnorm_backward(const NormBackwardArgs& a, hipStream_t stream
         if (e != hipSuccess) return e;
     }
     if (a.dw) {
-        const dim3 grid(static_cast<uint32_t>((c + kDwCols - 1) / kDwCols));
-        rmsnorm_dw_kernel<<<grid, kDwCols * kDwGroups, 0, stream>>>(a.parts, parts, c, a.dw,
-                                                                    a.dw_dtype);
+        auto run = [&](auto kernel, int per) {
+            kernel<<<static_cast<uint32_t>((c + per - 1) / per), kDwThreads, 0, stream>>>(
+                a.parts, parts, c, a.dw, a.dw_dtype);
+        };
+        if (c <= 2048) run(rmsnorm_dw_kernel<32>, 32);
+        else run(rmsnorm_dw_kernel<64>, 64);
         return hipGetLastError();
     }
     return hipSuccess;

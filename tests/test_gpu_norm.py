@@ -283,3 +283,45 @@ def test_norm_calls_in_a_graph_and_on_another_stream():
         assert all(torch.equal(a, b) for a, b in zip(outs, want)), k
         both()
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("rows,cols", [(8200, 1001), (4100, 7), (4100, 15), (2100, 2047),
+                                       (2100, 1024)])
+def test_backward_of_many_narrow_rows(rows, cols):
+    """More partial rows of dw than CUs; rows with and without a last eight."""
+    dev = device()
+    dy, h = _randn(1, rows, cols, dtype=BF16), _randn(2, rows, cols, dtype=F16)
+    w, rstd = _randn(3, cols, dtype=F16), 1 + 0.1 * _randn(4, rows)
+    dx, dw = torch.empty_like(dy), torch.empty(cols, device=dev)
+    ws = torch.empty(zs.zero_rmsnorm_backward_workspace(rows, cols), dtype=torch.uint8, device=dev)
+    zs.zero_rmsnorm_backward(dy, h, w, rstd, dx, dw, ws)
+    wx, ww = ref.rmsnorm_backward(dy, h, w, rstd, None)
+    _assert_backward(dx, dw, wx, ww, dy, h, w, rstd, None)
+
+
+@pytest.mark.parametrize("rows,cols", [(600, 5), (600, 9), (300, 5001), (260, 8185), (20, 9003),
+                                       (3, 17001)])
+def test_backward_in_place_where_rows_end_inside_a_pack(rows, cols):
+    """A row's last pack repeats elements of the one before: in place too the
+    same bits, and an inf among them stays in its row and column."""
+    dev = device()
+    dy, h, dres = (_randn(k, rows, cols, dtype=F16) for k in (1, 2, 3))
+    w, rstd = _randn(4, cols, dtype=F16), 1 + 0.1 * _randn(5, rows)
+    ws = torch.empty(zs.zero_rmsnorm_backward_workspace(rows, cols), dtype=torch.uint8, device=dev)
+    dx, dw, dw2 = torch.empty_like(dy), torch.empty_like(w), torch.empty_like(w)
+    zs.zero_rmsnorm_backward(dy, h, w, rstd, dx, dw, ws, dres=dres)
+    wx, ww = ref.rmsnorm_backward(dy, h, w, rstd, dres)
+    _assert_backward(dx, dw, wx, ww, dy, h, w, rstd, dres)
+    for which in ("dres", "h", "dy"):
+        args = dict(dy=dy.clone(), h=h.clone(), dres=dres.clone())
+        out = args[which]
+        zs.zero_rmsnorm_backward(args["dy"], args["h"], w, rstd, out, dw2, ws, dres=args["dres"])
+        assert torch.equal(out, dx) and torch.equal(dw, dw2), which
+    bad = dy.clone()
+    bad[1, cols - 4] = math.inf
+    out = torch.empty_like(dx)
+    zs.zero_rmsnorm_backward(bad, h, w, rstd, out, dw2, ws, dres=dres)
+    others = torch.arange(rows, device=dev) != 1
+    assert torch.equal(out[others], dx[others]) and not torch.isfinite(out[1]).any()
+    ok = torch.arange(cols, device=dev) != cols - 4
+    assert torch.equal(dw2[ok], dw[ok]) and not torch.isfinite(dw2[cols - 4])
