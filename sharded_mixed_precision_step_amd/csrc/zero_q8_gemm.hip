@@ -444,10 +444,13 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void q8_gemm_kernel(const GemmArgs
 // ---- few rows --------------------------------------------------------------
 //
 // Up to 16 rows by 16 columns of c per workgroup, its eight waves sharing k: wave
-// w takes the steps w, w + 8, ..., straight from memory into registers (no byte
-// is used twice, so LDS would only add a stop), and the eight sums meet in LDS,
-// in wave order.  A pass over b, with everything in flight at once.
-constexpr int kSplit = 8, kSplitUnroll = 4;
+// w takes the steps 4 w .. 4 w + 3, 4 w + 32 .., straight from memory into
+// registers (no byte is used twice, so LDS would only add a stop), and the eight
+// sums meet in LDS, in wave order.  A pass over b, with everything in flight at
+// once.  Four neighbouring steps, for their scales then are one word: 16 x 4096 x
+// 4096 6.6 us, 7.8 with a byte per step (half of a load's cost is its lanes'
+// addresses; up to k = 640 the fewer waves cost 0.2).
+constexpr int kSplit = 8;
 
 __device__ __forceinline__ v8i load_fragment(Buffer base, uint32_t off, int at) {
     const u32x4 x = __builtin_bit_cast(
@@ -478,27 +481,28 @@ __global__ __launch_bounds__(64 * kSplit, 2) void q8_gemm_rows_kernel(const Gemm
     const int off_sa = static_cast<int>(row_a * static_cast<uint32_t>(a.ld_sa));
     const int off_sb = static_cast<int>(row_b * static_cast<uint32_t>(a.ld_sb));
     v4f acc = {0, 0, 0, 0};
-    auto some = [&](int k, auto count) {
-        constexpr int N = decltype(count)::value;
-        v8i fa[N], fb[N];
-        int ea[N], eb[N];
+    for (int k = 4 * wave; k < a.kblocks; k += 4 * kSplit) {
+        // the four steps' scales are a word, whose last bytes may be padding
+        const int ea = __builtin_amdgcn_raw_buffer_load_b32(buf_sa, off_sa, k, 0);
+        const int eb = __builtin_amdgcn_raw_buffer_load_b32(buf_sb, off_sb, k, 0);
+        const int last = a.kblocks - 1;
+        v8i fa[4], fb[4];
 #pragma unroll
-        for (int u = 0; u < N; ++u) {
-            const int at = k + u * kSplit;
-            fb[u] = load_fragment(buf_b, off_b, at * kStep);
-            fa[u] = load_fragment(buf_a, off_a, at * kStep);
-            eb[u] = __builtin_amdgcn_raw_buffer_load_b8(buf_sb, off_sb, at, 0);
-            ea[u] = __builtin_amdgcn_raw_buffer_load_b8(buf_sa, off_sa, at, 0);
+        for (int u = 0; u < 4; ++u) {
+            const int at = (k + u < last ? k + u : last) * kStep;
+            fb[u] = load_fragment(buf_b, off_b, at);
+            fa[u] = load_fragment(buf_a, off_a, at);
         }
-#pragma unroll
-        for (int u = 0; u < N; ++u)
-            acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb[u], fa[u], acc, FB, FA, 0,
-                                                                   eb[u], 0, ea[u]);
-    };
-    int k = wave;
-    for (; k + (kSplitUnroll - 1) * kSplit < a.kblocks; k += kSplitUnroll * kSplit)
-        some(k, std::integral_constant<int, kSplitUnroll>());
-    for (; k < a.kblocks; k += kSplit) some(k, std::integral_constant<int, 1>());
+        __builtin_amdgcn_sched_barrier(0);  // every load first
+#define ZERO_STEP(U)                                                                       \
+    if (k + U < a.kblocks)                                                                 \
+    acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb[U], fa[U], acc, FB, FA, U, eb, U, ea)
+        ZERO_STEP(0);
+        ZERO_STEP(1);
+        ZERO_STEP(2);
+        ZERO_STEP(3);
+#undef ZERO_STEP
+    }
     sums[wave][l] = acc;
     __syncthreads();
     if (wave != 0) return;
@@ -566,13 +570,13 @@ hipError_t gemm_formats(const GemmArgs& a, hipStream_t stream) {
 //   1024 x  4096    32   29   24   29         256 x 1024   39   19   21    8
 // A single round takes what its longest chain of loads takes: the large tiles
 // have the least traffic per product, the small ones are done soonest.
-// Up to 16 rows and 4,096 columns: the rows kernel, 7.9 us at 16 x 4096 against
-// 8.7 for 64 x 64 tiles (1 row: 5.9 against 8.4); at 16 x 14336 23 against 12,
-// where its 16-byte pieces of b cost more than they save.
+// Up to 16 rows and 8,192 columns, two workgroups a CU: the rows kernel, 6.7 us at
+// 16 x 4096 against 10.5 for 64 x 64 tiles, 10.6 at 16 x 8192 against 10.8; at
+// 16 x 14336 18 against 12, where its 16-byte pieces of b cost more than they save.
 enum Variant { kRowsKernel, kLarge, kMedium, kMediumEight, kSmall };
 
 Variant choose(int64_t m, int64_t n, int64_t steps) {
-    if (m <= 16 && n <= 4096) return kRowsKernel;
+    if (m <= 16 && n <= 8192) return kRowsKernel;
     auto tiles = [&](int64_t side) { return (m + side - 1) / side * ((n + side - 1) / side); };
     auto rounds = [&](int64_t side, int64_t at_once) {
         return (tiles(side) + at_once - 1) / at_once;

@@ -321,3 +321,29 @@ def test_gemm_repeats_bit_for_bit_on_streams_and_in_graphs():
         for (a, sa, b, sb, want), o in zip(cases, outs):
             assert torch.equal(want, o)
             zs.zero_q8_gemm(a, sa, b, sb, torch.empty_like(o))
+
+
+@pytest.mark.parametrize("m,n,steps", [(2400, 8100, s) for s in (33, 34, 35, 36)] +
+                         [(2560, 8192, 33)] + [(16, 8000, s) for s in (2, 3, 4, 5, 31, 36, 70)] +
+                         [(3, 100, s) for s in (29, 30, 63)])
+def test_gemm_of_shared_tiles_and_few_rows(m, n, steps):
+    """More tiles than CUs, so that some are shared by two workgroups, with rows
+    that end in a shared tile's first half (2400 = 9 x 256 + 96); few rows at
+    numbers of steps that leave a wave none, or a part of its four."""
+    dev = device()
+    k = 128 * steps - 77
+    print(f"case: gemm {m}x{n}x{k}", flush=True)
+    a, sa = _operand(m, k, E4, m, dev)
+    b, sb = _operand(n, k, E5, n, dev)
+    va, vb = ref.from_blocks(a, sa), ref.from_blocks(b, sb)
+    want = va @ vb.t()
+    tol = _gemm_tol(va, vb, sa, sb, torch.bfloat16, want)
+    base = torch.full((m + 2, n + 8), 7.0, dtype=torch.bfloat16, device=dev)
+    c = base[1:-1, :n]
+    zs.zero_q8_gemm(a, sa, b, sb, c)
+    ref.assert_close(c, want, tol, "c")
+    assert (base[0] == 7).all() and (base[-1] == 7).all() and (base[:, n:] == 7).all()
+    ones = torch.ones(m, n, device=dev)
+    zs.zero_q8_gemm(a, sa, b, sb, ones, accumulate=True)
+    tol = _gemm_tol(va, vb, sa, sb, torch.float32, want + 1, torch.ones_like(want))
+    ref.assert_close(ones, want + 1, tol, "added to c")
