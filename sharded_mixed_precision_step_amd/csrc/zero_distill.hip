@@ -343,13 +343,24 @@ __global__ __launch_bounds__(T, 4) void distill_kernel(const DistillArgs a) {
 template <int DT, DistillMode MODE>
 void distill_size(const DistillArgs& a, hipStream_t stream) {
     const dim3 grid(static_cast<uint32_t>(a.rows));
-    // Lanes per row: 256 where they hold it (37 rows of 32,001: 9.1 us held by 1,024,
-    // 14.7 us in two passes).  Two passes in one call: 1,024 lanes, so that fewer
-    // rows wait in the cache (4096 x 131072: 433 us, 489 with 512); one pass: 512
-    // (2048 x 50001, both calls: 134 us, 174 with 1,024, before streaming stores).
+    // Lanes per row: 256, else 512, where they hold it (37 rows of 32,001: 9.1 us held
+    // by 1,024, 14.7 in two passes; 16384 of 10,000: 168 held by 512, 275 by 1,024;
+    // the gradient alone 118, 134 in passes of single packs; the loss alone 116 and
+    // 110, where holding gains nothing).  Two passes in one call: 1,024 lanes, so
+    // that fewer rows wait in the cache (4096 x 131072: 433 us, 489 with 512); one
+    // pass: 512 (2048 x 50001, both calls: 134 us, 174 with 1,024, before streaming
+    // stores).
     if (a.vocab <= 256 * kUnroll * 8) {
         distill_kernel<DT, 256, kUnroll, MODE><<<grid, 256, 0, stream>>>(a);
-    } else if constexpr (MODE == kDistillBoth) {
+        return;
+    }
+    if constexpr (MODE != kDistillForward) {
+        if (a.vocab <= 512 * kUnroll * 8) {
+            distill_kernel<DT, 512, kUnroll, MODE><<<grid, 512, 0, stream>>>(a);
+            return;
+        }
+    }
+    if constexpr (MODE == kDistillBoth) {
         if (a.vocab <= 1024 * kUnroll * 8)
             distill_kernel<DT, 1024, kUnroll, MODE><<<grid, 1024, 0, stream>>>(a);
         else distill_kernel<DT, 1024, 0, MODE><<<grid, 1024, 0, stream>>>(a);

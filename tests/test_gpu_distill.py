@@ -266,3 +266,26 @@ def test_distill_teacher_logits_of_the_lowest_value(tau, tdtype, two):
     want = _run(logits, index, same, tau, weight, 64.0, two)
     assert all(torch.equal(x, y) for x, y in zip(got, want))
     _check(logits, index, same, tau, weight, 64.0, two)
+
+
+@pytest.mark.parametrize("two", [False, True])
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+@pytest.mark.parametrize("rows,vocab,top", [(19, 8200, 70), (3, 12345, 1000), (5, 16384, 3),
+                                            (4, 16385, 600)])
+def test_distill_of_rows_that_512_lanes_hold(rows, vocab, top, dtype, two):
+    """And the first that they do not; in the logits' place too, at an odd
+    address."""
+    device()
+    logits, index, teacher, weight = _case(rows, vocab, top, dtype, F32, torch.int64)
+    _check(logits, index, teacher, 1.5, weight, 512.0, two)
+    base = torch.empty(rows, vocab + 3, dtype=dtype, device="cuda")
+    base[:, 1:1 + vocab] = logits
+    want = _run(logits, index, teacher, 1.5, weight, 512.0, two)
+    own = base[:, 1:1 + vocab]
+    loss, lse = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+    zs.zero_distill(own, index, teacher, loss, lse, own, temperature=1.5, row_weight=weight,
+                    loss_scale=512.0)
+    tl, te, tg = _tols(logits, index, teacher, 1.5, weight, 512.0,
+                       *(x.double() for x in want))
+    ref.assert_close(own, want[2].double(), 2 * tg, "grad in place")
+    ref.assert_close(loss, want[0].double(), 2 * tl, "loss")
