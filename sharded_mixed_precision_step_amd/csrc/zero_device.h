@@ -82,6 +82,48 @@ __device__ __forceinline__ Raw8<BYTES> load8(const void* p, int64_t i, int n) {
     return r;
 }
 
+// Elements c .. c + 7 of the row of cols elements that starts at element `row` of
+// p.  RAGGED, for eight columns or more: without a wait at the row's end, where
+// the row's last eight are loaded, and settle8 moves them into place once they
+// are needed.  What that loads of the pack before is dropped, so that it does not
+// matter if its owner has written there meanwhile.
+template <int BYTES, bool RAGGED>
+__device__ __forceinline__ Raw8<BYTES> load8_row(const void* p, int64_t row, int c, int cols) {
+    if constexpr (!RAGGED) return load8<BYTES>(p, row + c, cols - c);
+    else return load8<BYTES>(p, row + (c < cols - 8 ? c : cols - 8), 8);
+}
+template <int BYTES, bool RAGGED>
+__device__ __forceinline__ void settle8(Raw8<BYTES>& r, int c, int cols) {
+    if constexpr (!RAGGED) return;
+    const int back = c + 8 - cols;        // places that the elements lie too early
+    if (__ballot(back > 0) == 0) return;  // a branch: most waves have no row's end
+    constexpr int kWords = BYTES == 4 ? 8 : 4;
+    const int words = BYTES == 4 ? back : back >> 1;
+    uint32_t w[kWords];
+#pragma unroll
+    for (int k = 0; k < kWords; ++k) w[k] = r.v[k / 4][k % 4];
+#pragma unroll
+    for (int d = 1; d < kWords; d *= 2) {
+#pragma unroll
+        for (int k = 0; k < kWords; ++k) {
+            const uint32_t from = k + d < kWords ? w[k + d < kWords ? k + d : 0] : 0;
+            w[k] = words & d ? from : w[k];
+        }
+    }
+    if constexpr (BYTES == 2) {
+#pragma unroll
+        for (int k = 0; k < kWords; ++k) {
+            const uint32_t above = k + 1 < kWords ? w[k + 1 < kWords ? k + 1 : 0] : 0;
+            w[k] = back & 1 ? w[k] >> 16 | above << 16 : w[k];
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < kWords; ++k) {
+        const uint32_t moved = back < 8 ? w[k] : 0;
+        r.v[k / 4][k % 4] = back > 0 ? moved : r.v[k / 4][k % 4];
+    }
+}
+
 template <int BYTES>
 __device__ __forceinline__ void widen8(const Raw8<BYTES>& r, bool bf16, float (&f)[8]) {
     if constexpr (BYTES == 4) {

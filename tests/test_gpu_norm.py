@@ -325,3 +325,33 @@ def test_backward_in_place_where_rows_end_inside_a_pack(rows, cols):
     assert torch.equal(out[others], dx[others]) and not torch.isfinite(out[1]).any()
     ok = torch.arange(cols, device=dev) != cols - 4
     assert torch.equal(dw2[ok], dw[ok]) and not torch.isfinite(dw2[cols - 4])
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+@pytest.mark.parametrize("rows,cols", [(600, 9), (300, 513), (300, 1028), (200, 4101), (40, 9001),
+                                       (9, 16383), (5, 16387)])
+def test_norm_in_place_where_rows_end_inside_a_pack(rows, cols, dtype):
+    """h in the residual's place and in x's, y in x's: the bits of a call with
+    arrays of its own, which is checked against the definition."""
+    dev = device()
+    x, res = _randn(1, rows, cols, dtype=dtype), _randn(2, rows, cols, dtype=dtype)
+    w = _randn(3, cols, dtype=F16)
+
+    def call(x, res, h, y):
+        q, s = zs.q8_empty(rows, cols)
+        zs.zero_rmsnorm(x, w, EPS, residual=res, h=h, y=y, q=q, s=s)
+        return q.view(torch.uint8), s.view(torch.uint8)
+
+    h, y = torch.empty_like(x), torch.empty_like(x)
+    q, s = call(x, res, h, y)
+    wh, _, wy = ref.rmsnorm(x, res, w, EPS)
+    ref.assert_close(h, wh, ref.half_step(dtype, wh) + U * wh.abs(), "h")
+    # the mean of squares: 24 terms a lane and 22 joins; sqrt, division and two products
+    ref.assert_close(y, wy, ref.half_step(dtype, wy) + 100 * U * wy.abs(), "y")
+    for h_in, y_in in (("res", None), ("x", None), ("res", "x"), (None, "x")):
+        a = dict(x=x.clone(), res=res.clone())
+        own_h, own_y = torch.empty_like(x), torch.empty_like(x)
+        got_h, got_y = a.get(h_in, own_h), a.get(y_in, own_y)
+        got = call(a["x"], a["res"], got_h, got_y)
+        assert torch.equal(got_h, h) and torch.equal(got_y, y), (h_in, y_in)
+        assert torch.equal(got[0], q) and torch.equal(got[1], s), (h_in, y_in)
