@@ -11,7 +11,8 @@
 // on a grid of 2^-13 of the largest one's power of two, truncating, and join the
 // eights in fp32.  On normally distributed values that is 1.3e-5 of the result
 // (2-norm), a fifteenth of an fp16 rounding; the instructions that keep more do
-// half the work per cycle.
+// half the work per cycle.  Up to 16 rows, where memory bounds the product, they
+// are the ones used (see "few rows").
 //
 // Large products are bound by the matrix cores at the clock their power allows:
 // 8192 x 14336 x 4096 in 256 x 256 tiles takes 380 us, 2.5 PFLOP/s, with the
@@ -450,6 +451,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void q8_gemm_kernel(const GemmArgs
 // once.  Four neighbouring steps, for their scales then are one word: 16 x 4096 x
 // 4096 6.6 us, 7.8 with a byte per step (half of a load's cost is its lanes'
 // addresses; up to k = 640 the fewer waves cost 0.2).
+//
+// Memory bounds it, so the products go through the bf16 instructions, which keep
+// them whole and sum in fp32, and a block's scales are applied to its sum: 6e-8 of
+// the result, where the scaled 8-bit instructions reach 2e-5 in 0.2 us less.
 constexpr int kSplit = 8;
 
 __device__ __forceinline__ v8i load_fragment(Buffer base, uint32_t off, int at) {
@@ -464,6 +469,44 @@ __device__ __forceinline__ v8i load_fragment(Buffer base, uint32_t off, int at) 
         r[k + 4] = static_cast<int>(y[k]);
     }
     return r;
+}
+
+typedef __bf16 v8b __attribute__((ext_vector_type(8)));
+
+// Eight 8-bit floats as bf16, which holds each of them exactly.
+template <int FMT>
+__device__ __forceinline__ v8b widen(int lo, int hi) {
+    v2b r[4];
+    if constexpr (FMT == ZERO_E4M3) {
+        r[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false);
+        r[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true);
+        r[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false);
+        r[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true);
+    } else {
+        r[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(lo, 1.0f, false);
+        r[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(lo, 1.0f, true);
+        r[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(hi, 1.0f, false);
+        r[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(hi, 1.0f, true);
+    }
+    return v8b{r[0][0], r[0][1], r[1][0], r[1][1], r[2][0], r[2][1], r[3][0], r[3][1]};
+}
+
+// acc += 2^(ea + eb) times a block's products.
+template <int FA, int FB>
+__device__ __forceinline__ void add_block(const v8i& fa, const v8i& fb, uint32_t ea,
+                                          const int (&eb)[4], int shift, v4f& acc) {
+    v4f sum = {0, 0, 0, 0};
+#pragma unroll
+    for (int p = 0; p < 8; p += 2)
+        sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen<FB>(fb[p], fb[p + 1]),
+                                                      widen<FA>(fa[p], fa[p + 1]), sum, 0, 0, 0);
+    const uint32_t a = ea >> shift & 255u;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const uint32_t b = static_cast<uint32_t>(eb[r]) >> shift & 255u;
+        const float x = a == 255u || b == 255u ? __builtin_nanf("") : sum[r];
+        acc[r] += __builtin_ldexpf(x, static_cast<int>(a + b) - 254);
+    }
 }
 
 template <int FA, int FB>
@@ -494,14 +537,13 @@ __global__ __launch_bounds__(64 * kSplit, 2) void q8_gemm_rows_kernel(const Gemm
             fa[u] = load_fragment(buf_a, off_a, at);
         }
         __builtin_amdgcn_sched_barrier(0);  // every load first
-#define ZERO_STEP(U)                                                                       \
-    if (k + U < a.kblocks)                                                                 \
-    acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb[U], fa[U], acc, FB, FA, U, eb, U, ea)
-        ZERO_STEP(0);
-        ZERO_STEP(1);
-        ZERO_STEP(2);
-        ZERO_STEP(3);
-#undef ZERO_STEP
+        // a lane's sums belong to b's rows 4 (l / 16) .. + 3, a's row l % 16
+        int scale_b[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) scale_b[r] = __shfl(eb, 4 * (l / 16) + r);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (k + u < a.kblocks) add_block<FA, FB>(fa[u], fb[u], ea, scale_b, 8 * u, acc);
     }
     sums[wave][l] = acc;
     __syncthreads();

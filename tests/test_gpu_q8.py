@@ -347,3 +347,37 @@ def test_gemm_of_shared_tiles_and_few_rows(m, n, steps):
     zs.zero_q8_gemm(a, sa, b, sb, ones, accumulate=True)
     tol = _gemm_tol(va, vb, sa, sb, torch.float32, want + 1, torch.ones_like(want))
     ref.assert_close(ones, want + 1, tol, "added to c")
+
+
+@pytest.mark.parametrize("fa,fb", [(E4, E4), (E5, E4), (E4, E5), (E5, E5)])
+@pytest.mark.parametrize("m,n,k", [(1, 16, 128), (16, 300, 384), (5, 8192, 640), (16, 129, 4224)])
+def test_gemm_of_few_rows_sums_in_fp32(m, n, k, fa, fb):
+    """Whole numbers whose sums of magnitudes stay below 2^24 are added without
+    any rounding in fp32, in whatever order: a product of 2^16 beside products of
+    up to 64 in each of the first eights, scales of 1 and 2 on both sides."""
+    dev = device()
+    print(f"case: gemm {m}x{n}x{k} {fa} {fb}", flush=True)
+    va = torch.randint(-8, 9, (m, k), device=dev, generator=_gen(m + k)).double()
+    vb = torch.randint(-8, 9, (n, k), device=dev, generator=_gen(n + k)).double()
+    for b0 in range(0, min(k, 640), 8):
+        va[:, b0 + b0 // 8 % 8] = 256.0
+        vb[:, b0 + b0 // 8 % 8] = 256.0
+    a, b = va.float().to(fa), vb.float().to(fb)
+    assert torch.equal(a.double(), va) and torch.equal(b.double(), vb)
+    steps = k // 128
+    sa = torch.full((m, -(-steps // 4) * 4), 127, dtype=torch.uint8, device=dev)
+    sb = torch.full((n, sa.shape[1]), 127, dtype=torch.uint8, device=dev)
+    sa[:, :steps:2] += 1
+    sb[:, 1:steps:3] += 1
+    va, vb = ref.from_blocks(a, sa), ref.from_blocks(b, sb)
+    assert (va.abs() @ vb.abs().t()).max() < 2 ** 24
+    c = torch.empty(m, n, device=dev)
+    zs.zero_q8_gemm(a, sa, b, sb, c)
+    assert torch.equal(c.double(), va @ vb.t())
+    # a scale byte of 255 is NaN, and a NaN element is
+    sa[m - 1, 0] = 255
+    b.view(torch.uint8)[n // 2, 5] = 0x7f
+    zs.zero_q8_gemm(a, sa, b, sb, c)
+    want = torch.zeros(m, n, dtype=torch.bool, device=dev)
+    want[m - 1], want[:, n // 2] = True, True
+    assert torch.equal(torch.isnan(c), want)
