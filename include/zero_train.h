@@ -83,7 +83,8 @@ extern "C" {
  *                        of 128 along a column of src); both NULL: not written
  * At least one output is given.  Outputs must not overlap src or each other.
  * rows == 0 or cols == 0 is a valid call that writes what the layout then holds:
- * nothing.  Returns ZERO_OK, ZERO_EINVAL, ZERO_EALIGN or ZERO_EHIP.
+ * nothing.  Returns ZERO_OK, ZERO_EINVAL (also for more than 2^31 - 1 tiles of
+ * 128 x 128), ZERO_EALIGN or ZERO_EHIP.
  */
 int zero_q8_quantize(const void* src, int32_t dtype, int64_t rows, int64_t cols, int64_t ld_src,
                      int32_t fmt, void* q, int64_t ld_q, uint8_t* s, int64_t ld_s, void* qt,
@@ -133,7 +134,8 @@ int zero_q8_gemm(const void* a, int32_t fmt_a, int64_t ld_a, const uint8_t* sa, 
  *   y = h * rstd * weight
  * with h kept in fp32 for the norm.
  *
- *   x, x_dtype, ld_x           [rows][cols], 1 <= cols <= ZERO_NORM_MAX_COLS
+ *   x, x_dtype, ld_x           [rows][cols], 0 <= rows <= 2^31 - 1,
+ *                              1 <= cols <= ZERO_NORM_MAX_COLS
  *   residual, r_dtype, ld_r    [rows][cols], or NULL
  *   weight, w_dtype            [cols]
  *   eps                        finite, >= 0
@@ -223,7 +225,7 @@ typedef struct zero_distill_inputs {
     const void* top_index;   /* int32 or int64 [rows][top]                       */
     const void* top_logit;   /* [rows][top]                                      */
     const float* row_weight; /* fp32[rows], finite, or NULL: every weight is 1   */
-    int64_t rows;            /* >= 0                                             */
+    int64_t rows;            /* 0 .. 2^31 - 1                                    */
     int64_t vocab;           /* 1 .. 2^31 - 1                                    */
     int64_t ld_logits;       /* >= vocab                                         */
     int64_t ld_top;          /* >= top, of both top_index and top_logit          */

@@ -95,7 +95,7 @@ __device__ __forceinline__ void take(Stat& st, const Raw8<B> (&r)[N], bool bf16,
 // T lanes per row; R > 0: the row's body is at most R * T packs, and stays in
 // registers.
 template <int DT, int T, int R, DistillMode MODE>
-__global__ __launch_bounds__(T, 4) void distill_kernel(const DistillArgs a) {
+__global__ __launch_bounds__(T, 4) void distill_kernel(const DistillArgs a, int64_t first) {
     constexpr int B = DT == ZERO_F32 ? 4 : 2;
     constexpr bool bf16 = DT == ZERO_BF16, kHeld = R > 0;
     constexpr int kWaves = T / 64, kEntries = ZERO_DISTILL_MAX_TOP / T;
@@ -105,7 +105,7 @@ __global__ __launch_bounds__(T, 4) void distill_kernel(const DistillArgs a) {
     __shared__ float loss_part[kWaves];
     __shared__ int32_t bad_part[kWaves];
     const int t = threadIdx.x, wave = t / 64;
-    const int64_t row = blockIdx.x;
+    const int64_t row = first + blockIdx.x;
     const float weight = a.weight ? a.weight[row] : 1.0f;
     const int vocab = static_cast<int>(a.vocab);
     const char* x = static_cast<const char*>(a.logits) + row * a.ld * B;
@@ -341,8 +341,13 @@ __global__ __launch_bounds__(T, 4) void distill_kernel(const DistillArgs a) {
 }
 
 template <int DT, DistillMode MODE>
-void distill_size(const DistillArgs& a, hipStream_t stream) {
-    const dim3 grid(static_cast<uint32_t>(a.rows));
+hipError_t distill_size(const DistillArgs& a, hipStream_t stream) {
+    auto run = [&](auto kernel, uint32_t lanes) {
+        return in_launches(a.rows, lanes, [&](int64_t first, uint32_t grid) {
+            kernel<<<grid, lanes, 0, stream>>>(a, first);
+            return hipGetLastError();
+        });
+    };
     // Lanes per row: 256, else 512, where they hold it (37 rows of 32,001: 9.1 us held
     // by 1,024, 14.7 in two passes; 16384 of 10,000: 168 held by 512, 275 by 1,024;
     // the gradient alone 118, 134 in passes of single packs; the loss alone 116 and
@@ -350,39 +355,32 @@ void distill_size(const DistillArgs& a, hipStream_t stream) {
     // that fewer rows wait in the cache (4096 x 131072: 433 us, 489 with 512); one
     // pass: 512 (2048 x 50001, both calls: 134 us, 174 with 1,024, before streaming
     // stores).
-    if (a.vocab <= 256 * kUnroll * 8) {
-        distill_kernel<DT, 256, kUnroll, MODE><<<grid, 256, 0, stream>>>(a);
-        return;
-    }
+    if (a.vocab <= 256 * kUnroll * 8) return run(distill_kernel<DT, 256, kUnroll, MODE>, 256);
     if constexpr (MODE != kDistillForward) {
-        if (a.vocab <= 512 * kUnroll * 8) {
-            distill_kernel<DT, 512, kUnroll, MODE><<<grid, 512, 0, stream>>>(a);
-            return;
-        }
+        if (a.vocab <= 512 * kUnroll * 8) return run(distill_kernel<DT, 512, kUnroll, MODE>, 512);
     }
     if constexpr (MODE == kDistillBoth) {
         if (a.vocab <= 1024 * kUnroll * 8)
-            distill_kernel<DT, 1024, kUnroll, MODE><<<grid, 1024, 0, stream>>>(a);
-        else distill_kernel<DT, 1024, 0, MODE><<<grid, 1024, 0, stream>>>(a);
+            return run(distill_kernel<DT, 1024, kUnroll, MODE>, 1024);
+        return run(distill_kernel<DT, 1024, 0, MODE>, 1024);
     } else {
-        distill_kernel<DT, 512, 0, MODE><<<grid, 512, 0, stream>>>(a);
+        return run(distill_kernel<DT, 512, 0, MODE>, 512);
     }
 }
 
 template <DistillMode MODE>
-void distill_type(const DistillArgs& a, hipStream_t stream) {
-    if (a.dtype == ZERO_F32) distill_size<ZERO_F32, MODE>(a, stream);
-    else if (a.dtype == ZERO_F16) distill_size<ZERO_F16, MODE>(a, stream);
-    else distill_size<ZERO_BF16, MODE>(a, stream);
+hipError_t distill_type(const DistillArgs& a, hipStream_t stream) {
+    if (a.dtype == ZERO_F32) return distill_size<ZERO_F32, MODE>(a, stream);
+    if (a.dtype == ZERO_F16) return distill_size<ZERO_F16, MODE>(a, stream);
+    return distill_size<ZERO_BF16, MODE>(a, stream);
 }
 
 }  // namespace
 
 hipError_t launch_distill(const DistillArgs& a, DistillMode mode, hipStream_t stream) {
-    if (mode == kDistillForward) distill_type<kDistillForward>(a, stream);
-    else if (mode == kDistillBackward) distill_type<kDistillBackward>(a, stream);
-    else distill_type<kDistillBoth>(a, stream);
-    return hipGetLastError();
+    if (mode == kDistillForward) return distill_type<kDistillForward>(a, stream);
+    if (mode == kDistillBackward) return distill_type<kDistillBackward>(a, stream);
+    return distill_type<kDistillBoth>(a, stream);
 }
 
 }  // namespace zero

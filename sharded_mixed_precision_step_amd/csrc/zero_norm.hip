@@ -18,10 +18,10 @@ namespace {
 using namespace dev;
 
 template <int MAX_T, int P, int XB, int RB, bool RAGGED>
-__global__ __launch_bounds__(MAX_T) void rmsnorm_kernel(const NormArgs a) {
+__global__ __launch_bounds__(MAX_T) void rmsnorm_kernel(const NormArgs a, int64_t first) {
     __shared__ float part[16];
     const int T = static_cast<int>(blockDim.x);
-    const int64_t row = blockIdx.x;
+    const int64_t row = first + blockIdx.x;
     const int t = threadIdx.x;
     Raw8<XB> rx[P];
     Raw8<RB == 0 ? 2 : RB> rr[P];
@@ -104,20 +104,22 @@ __global__ __launch_bounds__(MAX_T) void rmsnorm_kernel(const NormArgs a) {
 
 template <int MAX_T, int P, bool RAGGED = false>
 hipError_t norm_shape(const NormArgs& a, hipStream_t stream) {
-    const dim3 grid(static_cast<uint32_t>(a.rows));
-    const dim3 block(static_cast<uint32_t>((a.cols + P * 512 - 1) / (P * 512) * 64));
+    const uint32_t block = static_cast<uint32_t>((a.cols + P * 512 - 1) / (P * 512) * 64);
     const bool x4 = a.x_dtype == ZERO_F32, r4 = a.r_dtype == ZERO_F32;
-    if (!a.res) {
-        if (x4) rmsnorm_kernel<MAX_T, P, 4, 0, RAGGED><<<grid, block, 0, stream>>>(a);
-        else rmsnorm_kernel<MAX_T, P, 2, 0, RAGGED><<<grid, block, 0, stream>>>(a);
-    } else if (r4) {
-        if (x4) rmsnorm_kernel<MAX_T, P, 4, 4, RAGGED><<<grid, block, 0, stream>>>(a);
-        else rmsnorm_kernel<MAX_T, P, 2, 4, RAGGED><<<grid, block, 0, stream>>>(a);
-    } else {
-        if (x4) rmsnorm_kernel<MAX_T, P, 4, 2, RAGGED><<<grid, block, 0, stream>>>(a);
-        else rmsnorm_kernel<MAX_T, P, 2, 2, RAGGED><<<grid, block, 0, stream>>>(a);
-    }
-    return hipGetLastError();
+    auto run = [&](auto kernel) {
+        return in_launches(a.rows, block, [&](int64_t first, uint32_t grid) {
+            kernel<<<grid, block, 0, stream>>>(a, first);
+            return hipGetLastError();
+        });
+    };
+    if (!a.res)
+        return x4 ? run(rmsnorm_kernel<MAX_T, P, 4, 0, RAGGED>)
+                  : run(rmsnorm_kernel<MAX_T, P, 2, 0, RAGGED>);
+    if (r4)
+        return x4 ? run(rmsnorm_kernel<MAX_T, P, 4, 4, RAGGED>)
+                  : run(rmsnorm_kernel<MAX_T, P, 2, 4, RAGGED>);
+    return x4 ? run(rmsnorm_kernel<MAX_T, P, 4, 2, RAGGED>)
+              : run(rmsnorm_kernel<MAX_T, P, 2, 2, RAGGED>);
 }
 
 }  // namespace

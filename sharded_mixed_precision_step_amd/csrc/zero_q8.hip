@@ -69,12 +69,13 @@ __device__ __forceinline__ u32x2 convert(const Raw8<DT == ZERO_F32 ? 4 : 2>& r,
 
 template <int DT, int FMT, bool ROWS, bool COLS>
 __global__ __launch_bounds__(kThreads) void quantize_kernel(const QuantizeArgs a,
-                                                            uint32_t tiles_c) {
+                                                            uint32_t tiles_c, uint32_t first) {
     constexpr int B = DT == ZERO_F32 ? 4 : 2;
     const int t = threadIdx.x;
-    const uint32_t tile_r = blockIdx.x / tiles_c;  // 32-bit: both fit
+    const uint32_t tile = first + blockIdx.x;  // 32-bit: all of them fit
+    const uint32_t tile_r = tile / tiles_c;
     const int64_t r0 = static_cast<int64_t>(tile_r) * kTile;
-    const int64_t c0 = static_cast<int64_t>(blockIdx.x - tile_r * tiles_c) * kTile;
+    const int64_t c0 = static_cast<int64_t>(tile - tile_r * tiles_c) * kTile;
     const void* src = a.src[a.ctl ? (a.ctl->cur & 1) : 0];
     const int rows = static_cast<int>(a.rows - r0 < kTile ? a.rows - r0 : kTile);
     const int cols = static_cast<int>(a.cols - c0 < kTile ? a.cols - c0 : kTile);
@@ -210,17 +211,25 @@ __global__ __launch_bounds__(kThreads) void quantize_kernel(const QuantizeArgs a
 }
 
 template <int DT, int FMT>
-void quantize_forms(const QuantizeArgs& a, dim3 grid, uint32_t tiles_c, hipStream_t stream) {
-    if (!a.qt) quantize_kernel<DT, FMT, true, false><<<grid, kThreads, 0, stream>>>(a, tiles_c);
-    else if (!a.q)
-        quantize_kernel<DT, FMT, false, true><<<grid, kThreads, 0, stream>>>(a, tiles_c);
-    else quantize_kernel<DT, FMT, true, true><<<grid, kThreads, 0, stream>>>(a, tiles_c);
+hipError_t quantize_forms(const QuantizeArgs& a, hipStream_t stream) {
+    const uint32_t tiles_c = static_cast<uint32_t>((a.cols + kTile - 1) / kTile);
+    auto run = [&](auto kernel) {
+        return in_launches(quantize_blocks(a.rows, a.cols), kThreads,
+                           [&](int64_t first, uint32_t grid) {
+                               kernel<<<grid, kThreads, 0, stream>>>(
+                                   a, tiles_c, static_cast<uint32_t>(first));
+                               return hipGetLastError();
+                           });
+    };
+    if (!a.qt) return run(quantize_kernel<DT, FMT, true, false>);
+    if (!a.q) return run(quantize_kernel<DT, FMT, false, true>);
+    return run(quantize_kernel<DT, FMT, true, true>);
 }
 
 template <int DT>
-void quantize_type(const QuantizeArgs& a, dim3 grid, uint32_t tiles_c, hipStream_t stream) {
-    if (a.fmt == ZERO_E4M3) quantize_forms<DT, ZERO_E4M3>(a, grid, tiles_c, stream);
-    else quantize_forms<DT, ZERO_E5M2>(a, grid, tiles_c, stream);
+hipError_t quantize_type(const QuantizeArgs& a, hipStream_t stream) {
+    return a.fmt == ZERO_E4M3 ? quantize_forms<DT, ZERO_E4M3>(a, stream)
+                              : quantize_forms<DT, ZERO_E5M2>(a, stream);
 }
 
 }  // namespace
@@ -230,12 +239,9 @@ int64_t quantize_blocks(int64_t rows, int64_t cols) {
 }
 
 hipError_t launch_q8_quantize(const QuantizeArgs& a, hipStream_t stream) {
-    const dim3 grid(static_cast<uint32_t>(quantize_blocks(a.rows, a.cols)));
-    const uint32_t tiles_c = static_cast<uint32_t>((a.cols + kTile - 1) / kTile);
-    if (a.dtype == ZERO_F32) quantize_type<ZERO_F32>(a, grid, tiles_c, stream);
-    else if (a.dtype == ZERO_F16) quantize_type<ZERO_F16>(a, grid, tiles_c, stream);
-    else quantize_type<ZERO_BF16>(a, grid, tiles_c, stream);
-    return hipGetLastError();
+    if (a.dtype == ZERO_F32) return quantize_type<ZERO_F32>(a, stream);
+    if (a.dtype == ZERO_F16) return quantize_type<ZERO_F16>(a, stream);
+    return quantize_type<ZERO_BF16>(a, stream);
 }
 
 }  // namespace zero

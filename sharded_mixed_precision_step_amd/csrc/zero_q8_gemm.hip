@@ -642,6 +642,30 @@ Variant choose(int64_t m, int64_t n, int64_t steps) {
 int64_t gemm_tiles(int64_t m, int64_t n) { return (m + 63) / 64 * ((n + 63) / 64); }
 
 hipError_t launch_q8_gemm(const GemmArgs& a, hipStream_t stream) {
+    // HIP launches fewer than 2^32 lanes: 256 for a tile of 64 x 64, or 512 for
+    // one of 128 x 128, which may be two of those.  A larger c in halves of its
+    // longer side, cut at a border of every tile.
+    constexpr int64_t kLaunchTiles = int64_t{1} << 23;
+    if (gemm_tiles(a.m, a.n) > kLaunchTiles) {
+        GemmArgs one = a, two = a;
+        const int64_t half = ((a.m > a.n ? a.m : a.n) / 2 + 255) / 256 * 256;
+        int64_t elements = half;
+        if (a.m > a.n) {
+            one.m = half;
+            two.m = a.m - half;
+            two.a += half * a.ld_a;
+            two.sa += half * a.ld_sa;
+            elements *= a.ld_c;
+        } else {
+            one.n = half;
+            two.n = a.n - half;
+            two.b += half * a.ld_b;
+            two.sb += half * a.ld_sb;
+        }
+        two.c = static_cast<char*>(a.c) + elements * (a.c_dtype == ZERO_F32 ? 4 : 2);
+        const hipError_t e = launch_q8_gemm(one, stream);
+        return e == hipSuccess ? launch_q8_gemm(two, stream) : e;
+    }
     switch (choose(a.m, a.n, a.kblocks)) {
         case kRowsKernel: return gemm_rows(a, stream);
         case kLarge: return gemm_formats<256, 256, 2, 4, 2, true>(a, stream);

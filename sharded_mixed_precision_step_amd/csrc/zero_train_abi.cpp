@@ -14,7 +14,7 @@ using zero::hip_fail;
 using zero::ok;
 using zero::overlap;
 
-constexpr int64_t kMaxGrid = 0x7fffffff;   // workgroups of one launch
+constexpr int64_t kMaxGrid = 0x7fffffff;   // workgroups of one call, in one launch or several
 constexpr int64_t kMaxTiles = int64_t{1} << 27;  // a band of eight rows of them fits 32 bits
 constexpr int64_t kMaxBytes = int64_t{1} << 56;
 
@@ -129,7 +129,7 @@ int quantize(const void* const* srcs, int n_srcs, int32_t dtype, int64_t rows, i
     }
     if ((rc = check_apart(out, n_out, in, n_srcs, who))) return rc;
     if (zero::quantize_blocks(rows, cols) > kMaxGrid)
-        return fail(ZERO_EINVAL, "%s: the matrix is larger than one launch covers", who);
+        return fail(ZERO_EINVAL, "%s: the matrix is larger than a call's launches cover", who);
     zero::QuantizeArgs a = {};
     a.src[0] = srcs[0];
     a.src[1] = n_srcs > 1 ? srcs[1] : nullptr;
@@ -216,7 +216,7 @@ int distill(const zero_distill_inputs* in, zero::DistillMode mode, float loss_sc
     }
     if ((rc = check_apart(outs, n_out, ins, n_in, who))) return rc;
     if (in->rows > kMaxGrid)
-        return fail(ZERO_EINVAL, "%s: more rows than one launch covers", who);
+        return fail(ZERO_EINVAL, "%s: more rows than a call's launches cover", who);
     zero::DistillArgs a = {};
     a.logits = in->logits; a.index = in->top_index; a.top_logit = in->top_logit;
     a.weight = in->row_weight;
@@ -300,7 +300,7 @@ int zero_q8_gemm(const void* a, int32_t fmt_a, int64_t ld_a, const uint8_t* sa, 
     g.fmt_a = fmt_a; g.fmt_b = fmt_b; g.c_dtype = c_dtype; g.accumulate = accumulate;
     g.c = c; g.ld_c = ld_c;
     if (zero::gemm_tiles(m, n) > kMaxTiles)
-        return fail(ZERO_EINVAL, "%s: c is larger than one launch covers", who);
+        return fail(ZERO_EINVAL, "%s: c is larger than a call's launches cover", who);
     const hipError_t e = zero::launch_q8_gemm(g, static_cast<hipStream_t>(stream));
     return e == hipSuccess ? ok() : hip_fail(e, who);
 }
@@ -360,7 +360,7 @@ int zero_rmsnorm(const void* x, int32_t x_dtype, int64_t ld_x, const void* resid
         }
     }
     if ((rc = check_apart(outs, n_out, nullptr, 0, who))) return rc;
-    if (rows > kMaxGrid) return fail(ZERO_EINVAL, "%s: more rows than one launch covers", who);
+    if (rows > kMaxGrid) return fail(ZERO_EINVAL, "%s: more rows than a call's launches cover", who);
     zero::NormArgs a = {};
     a.x = x; a.res = residual; a.weight = weight;
     a.ld_x = ld_x; a.ld_r = ld_r; a.ld_h = ld_h; a.ld_y = ld_y; a.ld_q = ld_q; a.ld_s = ld_s;

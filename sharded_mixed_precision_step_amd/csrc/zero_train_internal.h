@@ -10,6 +10,20 @@
 
 namespace zero {
 
+// HIP launches fewer than 2^32 lanes along a dimension.  Workgroups 0 ..
+// blocks - 1 of `lanes` lanes each, in as many launches as that takes:
+// launch(first, n) launches n of them from `first` on.
+template <class Launch>
+inline hipError_t in_launches(int64_t blocks, int64_t lanes, Launch launch) {
+    const int64_t most = 0xffffffff / lanes;
+    for (int64_t first = 0; first < blocks; first += most) {
+        const int64_t left = blocks - first;
+        const hipError_t e = launch(first, static_cast<uint32_t>(left < most ? left : most));
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
 struct QuantizeArgs {
     const void* src[2];               // the copy cur picks; src[0] without a control block
     const zero_step_control* ctl;     // or NULL
