@@ -114,6 +114,15 @@ struct Turn {
     }
 };
 
+// Between what a wave's lanes write to LDS and what its other lanes read there,
+// and the other way round: an order that the compiler keeps.  No instruction: LDS
+// takes a wave's accesses as they come.
+__device__ __forceinline__ void wave_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // From there, kRows rows at a time: whole rows of a 16-bit type, written.
 template <int COLS, int DTYPE>
 __device__ __forceinline__ void put_rows(const GemmArgs& a, int64_t row0, int64_t col0,
@@ -406,10 +415,12 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& a, int64_t m0, int64_t
                 *Out::at(turn, l % 32, 8 * j + 2 * r + l / 32) =
                     v4f{acc[i][j][4 * r], acc[i][j][4 * r + 1], acc[i][j][4 * r + 2],
                         acc[i][j][4 * r + 3]};
+        wave_fence();
         const int64_t row = m0 + row_a + 32 * i, col = n0 + row_b;
         if (plain && a.c_dtype == ZERO_F16) put_rows<32 * NI, ZERO_F16>(a, row, col, turn);
         else if (plain) put_rows<32 * NI, ZERO_BF16>(a, row, col, turn);
         else put_any<32 * NI>(a, row, col, turn);
+        wave_fence();  // the next rows take the same place
     }
 }
 
