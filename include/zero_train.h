@@ -118,10 +118,11 @@ int zero_q8_quantize_ctl(const void* const* srcs_fp16, int64_t rows, int64_t col
  *                 in fp32 and rounded once)
  * With x [t][k], w [n][k] and dy [t][n] the products of a linear layer are
  * y = x w^T (a = x, b = w), dx = dy w (a = dy, b = w transposed) and
- * dw = dy^T x (a = dy transposed, b = x transposed).  k == 0 gives zeros.
- * c must not overlap a, b or their scales.  Returns ZERO_OK, ZERO_EINVAL,
- * ZERO_EALIGN, ZERO_ERANGE (k or a row stride above ZERO_Q8_MAX_LD) or ZERO_EHIP;
- * ZERO_EINVAL also for a c of more than 2^27 tiles of 64 x 64.
+ * dw = dy^T x (a = dy transposed, b = x transposed).  k == 0 gives zeros,
+ * whatever a, b, their scales and strides are.  c must not overlap a, b or their
+ * scales.  Returns ZERO_OK, ZERO_EINVAL, ZERO_EALIGN, ZERO_ERANGE (k or a row
+ * stride above ZERO_Q8_MAX_LD) or ZERO_EHIP; ZERO_EINVAL also for a c of more
+ * than 2^27 tiles of 64 x 64.
  */
 int zero_q8_gemm(const void* a, int32_t fmt_a, int64_t ld_a, const uint8_t* sa, int64_t ld_sa,
                  const void* b, int32_t fmt_b, int64_t ld_b, const uint8_t* sb, int64_t ld_sb,

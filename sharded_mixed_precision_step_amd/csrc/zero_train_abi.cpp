@@ -282,6 +282,11 @@ int zero_q8_gemm(const void* a, int32_t fmt_a, int64_t ld_a, const uint8_t* sa, 
     if (accumulate != 0 && accumulate != 1)
         return fail(ZERO_EINVAL, "%s: accumulate = %d is neither 0 nor 1", who, accumulate);
     if (m == 0 || n == 0) return ok();
+    if (k == 0) {  // nothing of a and b is there
+        a = b = nullptr;
+        sa = sb = nullptr;
+        ld_a = ld_b = ld_sa = ld_sb = 0;
+    }
     if (k > ZERO_Q8_MAX_LD || ld_a > ZERO_Q8_MAX_LD || ld_b > ZERO_Q8_MAX_LD ||
         ld_sa > ZERO_Q8_MAX_LD || ld_sb > ZERO_Q8_MAX_LD)
         return fail(ZERO_ERANGE, "%s: k or a row stride is above %d", who, ZERO_Q8_MAX_LD);

@@ -381,3 +381,16 @@ def test_gemm_of_few_rows_sums_in_fp32(m, n, k, fa, fb):
     want = torch.zeros(m, n, dtype=torch.bool, device=dev)
     want[m - 1], want[:, n // 2] = True, True
     assert torch.equal(torch.isnan(c), want)
+
+
+@pytest.mark.parametrize("m,n", [(3, 50), (300, 70)])
+def test_gemm_of_no_columns_takes_empty_operands(m, n):
+    """The q8 matrices that q8_empty makes for k = 0."""
+    dev = device()
+    a, b = zs.q8_empty(m, 0), zs.q8_empty(n, 0)
+    zs.zero_q8_quantize(torch.empty(m, 0, device=dev), *a)
+    c = torch.full((m, n), 3.0, dtype=torch.float16, device=dev)
+    zs.zero_q8_gemm(*a, *b, c, accumulate=True)
+    assert (c == 3).all()
+    zs.zero_q8_gemm(*a, *b, c)
+    assert (c == 0).all()

@@ -257,3 +257,10 @@ def test_the_binding_refuses_host_and_mismatched_tensors():
                                 torch.zeros(4), None)
     assert zs.q8_shape(5, 0) == ((5, 0), (5, 0))
     assert zs.q8_shape(5, 129) == ((5, 256), (5, 4)) and zs.q8_shape(1, 640) == ((1, 640), (1, 8))
+
+
+def test_gemm_of_no_columns_asks_nothing_of_its_operands():
+    """k = 0: only c is looked at."""
+    none = dict(k=0, lda=1, ldsa=1, ldb=1, ldsb=1, a=None, sa=None, b=None, sb=None)
+    _refused(_gemm(**none, c=E + 1), EALIGN, "c is not")
+    _refused(_gemm(**dict(none, lda=-7, ldsb=1 << 40), ldc=19), EINVAL, "ld of c")
