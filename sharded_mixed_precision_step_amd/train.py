@@ -77,7 +77,9 @@ _declare()
 # short call's time is the host's.
 
 def _mat(t: torch.Tensor, kinds: dict, dev: torch.device, name: str) -> Tuple[int, int, int]:
-    """(pointer, type code, row stride) of a matrix on dev."""
+    """(pointer, type code, row stride) of a matrix on dev.  A single row's
+    stride says nothing: it counts as the row's length, rounded up to what the
+    q8 layout asks of strides."""
     code = kinds.get(t.dtype)
     if code is None:
         raise TypeError(f"{name} has dtype {t.dtype}")
@@ -87,12 +89,11 @@ def _mat(t: torch.Tensor, kinds: dict, dev: torch.device, name: str) -> Tuple[in
     if len(stride) != 2:
         raise ValueError(f"{name} has {len(stride)} dimensions, expected 2")
     ld, inner = stride
-    if inner != 1 or ld < t.shape[1]:
-        rows, cols = t.shape
-        if inner != 1 and cols > 1:
-            raise ValueError(f"the rows of {name} are not contiguous")
-        if rows <= 1:
-            ld = max(ld, cols)
+    rows, cols = t.shape
+    if inner != 1 and cols > 1:
+        raise ValueError(f"the rows of {name} are not contiguous")
+    if rows <= 1:
+        ld = (cols + 15) & -16
     return t.data_ptr(), code, ld
 
 
