@@ -318,7 +318,9 @@ __global__ __launch_bounds__(T, 4) void distill_kernel(const DistillArgs a, int6
         float kl = loss_part[0];
         for (int w = 1; w < kWaves; ++w) kl += loss_part[w];
         if (a.lse) a.lse[row] = lse;
-        if (a.loss) a.loss[row] = lse != lse ? lse : empty ? 0.0f : weight * a.tau * a.tau * kl;
+        // tau^2 may be below fp32's range where tau * kl is not
+        if (a.loss)
+            a.loss[row] = lse != lse ? lse : empty ? 0.0f : weight * a.tau * (a.tau * kl);
     }
     if constexpr (MODE != kDistillForward) {
         if (empty) return;

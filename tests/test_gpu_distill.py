@@ -289,3 +289,18 @@ def test_distill_of_rows_that_512_lanes_hold(rows, vocab, top, dtype, two):
                        *(x.double() for x in want))
     ref.assert_close(own, want[2].double(), 2 * tg, "grad in place")
     ref.assert_close(loss, want[0].double(), 2 * tl, "loss")
+
+
+@pytest.mark.parametrize("tau", [1e-19, 3e-22, 2.0 ** -100])
+def test_temperatures_whose_square_is_below_the_range(tau):
+    """One entry, p = 1, and a student whose softmax is one-hot, sum = 1: the loss
+    is w tau^2 (m - z) / tau.  1 / tau, the quotient, tau times it and the two
+    factors round, each by half a step: six roundings."""
+    logits, index, teacher, weight = _case(9, 3000, 1, F32, F32)
+    tau = float(torch.tensor(tau, dtype=F32))
+    loss = torch.full((9,), 7.0, device="cuda")
+    zs.zero_distill_forward(logits, index, teacher, loss, None, temperature=tau, row_weight=weight)
+    z = logits.double()
+    want = weight.double() * tau * (z.amax(1) - z.gather(1, index.long())[:, 0])
+    assert (want > 2.0 ** -120).all()
+    ref.assert_close(loss, want, 6.1 * U * want, "loss")
