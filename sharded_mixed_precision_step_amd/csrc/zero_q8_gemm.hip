@@ -461,11 +461,12 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void q8_gemm_kernel(const GemmArgs
 // sums meet in LDS, in wave order.  A pass over b, with everything in flight at
 // once.  Four neighbouring steps, for their scales then are one word: 16 x 4096 x
 // 4096 6.6 us, 7.8 with a byte per step (half of a load's cost is its lanes'
-// addresses; up to k = 640 the fewer waves cost 0.2).
+// addresses; up to k = 640 the fewer waves cost 0.2; both with the scaled 8-bit
+// instructions).
 //
 // Memory bounds it, so the products go through the bf16 instructions, which keep
 // them whole and sum in fp32, and a block's scales are applied to its sum: 6e-8 of
-// the result, where the scaled 8-bit instructions reach 2e-5 in 0.2 us less.
+// the result in 6.9 us, where the scaled 8-bit instructions reach 2e-5 in 6.7.
 constexpr int kSplit = 8;
 
 __device__ __forceinline__ v8i load_fragment(Buffer base, uint32_t off, int at) {
@@ -505,19 +506,22 @@ __device__ __forceinline__ v8b widen(int lo, int hi) {
 // acc += 2^(ea + eb) times a block's products.
 template <int FA, int FB>
 __device__ __forceinline__ void add_block(const v8i& fa, const v8i& fb, uint32_t ea,
-                                          const int (&eb)[4], int shift, v4f& acc) {
+                                          const uint32_t (&eb)[4], int shift, v4f& acc) {
     v4f sum = {0, 0, 0, 0};
 #pragma unroll
     for (int p = 0; p < 8; p += 2)
         sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen<FB>(fb[p], fb[p + 1]),
                                                       widen<FA>(fa[p], fa[p + 1]), sum, 0, 0, 0);
-    const uint32_t a = ea >> shift & 255u;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        const uint32_t b = static_cast<uint32_t>(eb[r]) >> shift & 255u;
-        const float x = a == 255u || b == 255u ? __builtin_nanf("") : sum[r];
-        acc[r] += __builtin_ldexpf(x, static_cast<int>(a + b) - 254);
-    }
+    for (int r = 0; r < 4; ++r)
+        acc[r] += __builtin_ldexpf(
+            sum[r], static_cast<int>((ea >> shift & 255u) + (eb[r] >> shift & 255u)) - 254);
+}
+
+// A byte of 255, a NaN for a scale, in one of the first n places of w.
+__device__ __forceinline__ bool nan_scale(uint32_t w, int n) {
+    if (n < 4) w &= (1u << 8 * n) - 1;
+    return ((w & 0x7f7f7f7fu) + 0x01010101u) & w & 0x80808080u;
 }
 
 template <int FA, int FB>
@@ -537,8 +541,8 @@ __global__ __launch_bounds__(64 * kSplit, 2) void q8_gemm_rows_kernel(const Gemm
     v4f acc = {0, 0, 0, 0};
     for (int k = 4 * wave; k < a.kblocks; k += 4 * kSplit) {
         // the four steps' scales are a word, whose last bytes may be padding
-        const int ea = __builtin_amdgcn_raw_buffer_load_b32(buf_sa, off_sa, k, 0);
-        const int eb = __builtin_amdgcn_raw_buffer_load_b32(buf_sb, off_sb, k, 0);
+        const uint32_t ea = __builtin_amdgcn_raw_buffer_load_b32(buf_sa, off_sa, k, 0);
+        const uint32_t eb = __builtin_amdgcn_raw_buffer_load_b32(buf_sb, off_sb, k, 0);
         const int last = a.kblocks - 1;
         v8i fa[4], fb[4];
 #pragma unroll
@@ -549,9 +553,15 @@ __global__ __launch_bounds__(64 * kSplit, 2) void q8_gemm_rows_kernel(const Gemm
         }
         __builtin_amdgcn_sched_barrier(0);  // every load first
         // a lane's sums belong to b's rows 4 (l / 16) .. + 3, a's row l % 16
-        int scale_b[4];
+        uint32_t scale_b[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) scale_b[r] = __shfl(eb, 4 * (l / 16) + r);
+        const int here = a.kblocks - k;
+        if (__ballot(nan_scale(ea, here) || nan_scale(eb, here))) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (nan_scale(ea, here) || nan_scale(scale_b[r], here)) acc[r] = __builtin_nanf("");
+        }
 #pragma unroll
         for (int u = 0; u < 4; ++u)
             if (k + u < a.kblocks) add_block<FA, FB>(fa[u], fb[u], ea, scale_b, 8 * u, acc);

@@ -381,6 +381,13 @@ def test_gemm_of_few_rows_sums_in_fp32(m, n, k, fa, fb):
     want = torch.zeros(m, n, dtype=torch.bool, device=dev)
     want[m - 1], want[:, n // 2] = True, True
     assert torch.equal(torch.isnan(c), want)
+    # ... unless its block lies behind k
+    if steps > 1:
+        sa[m - 1, 0], sa[:, steps - 1], sb[:, steps - 1] = 127, 255, 255
+        b.view(torch.uint8)[n // 2, 5] = 0
+        zs.zero_q8_gemm(a, sa, b, sb, c, k=k - 128)
+        va, vb = (ref.from_blocks(x, s)[:, :k - 128] for x, s in ((a, sa), (b, sb)))
+        assert torch.equal(c.double(), va @ vb.t())
 
 
 @pytest.mark.parametrize("m,n", [(3, 50), (300, 70)])
