@@ -151,7 +151,9 @@ int zero_q8_gemm(const void* a, int32_t fmt_a, int64_t ld_a, const uint8_t* sa, 
  * At least one of h, y, q and rstd is given.  Apart from the cases named, no
  * output may overlap an input or another output.  A row with a non-finite h
  * gives NaN, or inf, where the formula does; sums of squares are fp32's, so
- * that rows beyond 1.8e19, which no fp16 row is, count as infinitely long.
+ * that rows beyond 1.8e19, which no fp16 row is, count as infinitely long and
+ * squares of values below 1e-19 lose places, and below 2e-23 are zero (with
+ * eps == 0 such rows have an rstd of inf).
  * rows == 0 is a no-op.  Returns ZERO_OK, ZERO_EINVAL, ZERO_EALIGN, ZERO_ERANGE
  * (cols) or ZERO_EHIP.
  */

@@ -3,12 +3,14 @@
 // One workgroup per row.  The student's row goes by once for the running
 // maximum and sum of its softmax (fp32, from a finite start so that a row of
 // -inf stays countable) and once more for the gradient.  Rows of up to 32,768
-// elements stay in registers in between; longer ones are read twice, the second
-// time mostly from the memory-side cache, which the gradient's streaming stores
-// leave to them: 4096 x 131072 fp16 takes 429 us, 5.0 TB/s over the logits read
-// once and the gradient written once (494 us with ordinary stores, 524 us also
-// with half the loads under way; 751 us with the row held in 64 registers a lane,
-// where loading, summing and writing do not overlap).
+// elements stay in registers in between (16,384 where only the gradient is made,
+// 8,192 where only the loss is); longer ones are read twice, the second time mostly
+// from the memory-side cache, which the gradient's streaming stores leave to them:
+// 4096 x 131072 fp16 takes 463 us, 4.6 TB/s over the logits read once and the
+// gradient written once.  With a tenth of the rows of weight 0, 429 us (494 with
+// ordinary stores, 524 also with half the loads under way; 751 with the row held in
+// 64 registers a lane, where loading, summing and writing do not overlap).  fp32
+// logits: 2048 x 50001 203 us, 4.0 TB/s.
 //
 // The teacher's entries lie one to four per lane; their softmax joins across
 // the workgroup together with the row's, behind one barrier.  The gradient is

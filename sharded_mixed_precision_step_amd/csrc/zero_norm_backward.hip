@@ -64,6 +64,10 @@ __device__ __forceinline__ void load_weight(const NormBackwardArgs& a, int c, in
 // registers, and up to 8,192 the next one's loads are under way meanwhile (one
 // pack per lane: more waves for the arithmetic of the one row, 1003 x 5001 17 us
 // against 20 with two packs); wider rows are read again behind the reduction.
+// Those (and rows of less than 8 columns) also have more sums for dw and packs than
+// a lane's 128 registers hold, and spill: fp16, 1024 x 32768 132 us, 1.5 TB/s, 1024
+// x 65536 599.  Narrow rows leave lanes without elements, one wave to a row: 262144
+// x 128 201 us, 1.0 TB/s; 65536 x 256 56 us, 1.8.
 //
 // Where a row's length is no multiple of eight, a held row's last pack is its
 // last eight elements: what it shares with the pack before goes into the row's

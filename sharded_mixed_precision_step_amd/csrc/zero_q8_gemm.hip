@@ -15,8 +15,9 @@
 // are the ones used (see "few rows").
 //
 // Large products are bound by the matrix cores at the clock their power allows:
-// 8192 x 14336 x 4096 in 256 x 256 tiles takes 380 us, 2.5 PFLOP/s, with the
-// matrix cores at work in 64 % of the cycles and 1.8 GHz.  (Workgroups that go
+// 8192 x 14336 x 4096 in 256 x 256 tiles takes 383 us on a rested card and 396 to
+// 407 in a row, 2.4 to 2.5 PFLOP/s (402 to 441 where it is traced), with the matrix
+// cores at work in 64 % of the cycles and 1.8 GHz.  (Workgroups that go
 // through several tiles, one written while the next one's loads are under way,
 // gained 0 to 3 % and are not kept.)
 #include <type_traits>
@@ -142,7 +143,9 @@ __device__ __forceinline__ void put_rows(const GemmArgs& a, int64_t row0, int64_
         *reinterpret_cast<u32x4_any*>(to + r * T::kRows * a.ld_c) = v;
     }
 }
-// The same for any type, any part of a tile, and a sum with what is there.
+// The same for any type, any part of a tile, and a sum with what is there.  8192 x
+// 4096 x 4096 takes 106 us in fp16, 125 in fp32 or added to fp16, 157 added to fp32:
+// a row's old values are waited for before the next row's are asked for.
 template <int COLS>
 __device__ __forceinline__ void put_any(const GemmArgs& a, int64_t row0, int64_t col0,
                                         uint8_t* lds) {
@@ -466,7 +469,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void q8_gemm_kernel(const GemmArgs
 //
 // Memory bounds it, so the products go through the bf16 instructions, which keep
 // them whole and sum in fp32, and a block's scales are applied to its sum: 6e-8 of
-// the result in 6.9 us, where the scaled 8-bit instructions reach 2e-5 in 6.7.
+// the result in 7.0 us, where the scaled 8-bit instructions reach 2e-5 in 6.7.
 constexpr int kSplit = 8;
 
 __device__ __forceinline__ v8i load_fragment(Buffer base, uint32_t off, int at) {
@@ -633,9 +636,14 @@ hipError_t gemm_formats(const GemmArgs& a, hipStream_t stream) {
 //   1024 x  4096    32   29   24   29         256 x 1024   39   19   21    8
 // A single round takes what its longest chain of loads takes: the large tiles
 // have the least traffic per product, the small ones are done soonest.
-// Up to 16 rows and 8,192 columns, two workgroups a CU: the rows kernel, 6.7 us at
-// 16 x 4096 against 10.5 for 64 x 64 tiles, 10.6 at 16 x 8192 against 10.8; at
-// 16 x 14336 18 against 12, where its 16-byte pieces of b cost more than they save.
+// Beyond those sizes, of 22 with m from 17 or k up to 2^20 the choice is within 1 %
+// of the best of the four but for two (1024 x 4096 x 8192, 46.8 us for 43.5, and 2048
+// x 2048 x 14336, 84.5 for 74.5).  That best is far from what memory and the matrix
+// cores allow wherever there are fewer tiles than CUs, since a workgroup goes through
+// all of k: 17 to 100 x 4096 x 4096 take 11 to 12 us.
+// Up to 16 rows and 8,192 columns, two workgroups a CU: the rows kernel, 7.0 us at
+// 16 x 4096 x 4096 against 10.6 for 64 x 64 tiles, 10.8 at n = 8192 against 10.9; at
+// 14336 18 against 12.5, where its 16-byte pieces of b cost more than they save.
 enum Variant { kRowsKernel, kLarge, kMedium, kMediumEight, kSmall };
 
 Variant choose(int64_t m, int64_t n, int64_t steps) {
