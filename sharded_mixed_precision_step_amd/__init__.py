@@ -812,6 +812,27 @@ class DeviceStepper:
         zero_distill(logits, index, teacher, loss, lse, grad, temperature=temperature,
                      row_weight=row_weight, ctl=self.ctl, stream=stream)
 
+    def embed(self, copies, offset: int, vocab: int, cols: int, ids, y, *, scale: float = 1.0,
+              stream=None) -> None:
+        """zero_embed from the fp16 parameters the last single pass left current
+        (the previous ones if it was skipped): a [vocab, cols] table at
+        param_fp16[offset:], the copy picked on the device.  See zero_embed_ctl."""
+        end = offset + vocab * cols
+        params = [cp[3] for cp in copies]
+        for k, p in enumerate(params):
+            if offset < 0 or end > p.numel():
+                raise ValueError(f"table [{offset}, {end}) lies outside the {p.numel()} params "
+                                 f"of copy {k}")
+        zero_embed_ctl([p[offset:end].view(vocab, cols) for p in params], self.ctl, ids, y,
+                       scale=scale, stream=stream)
+
+    def logprob_backward(self, logits, ids, lse, dlogp, grad, *, entropy=None, dentropy=None,
+                         temperature: float = 1.0, stream=None) -> None:
+        """zero_logprob_backward with the loss scale of the next step, read on the
+        device, as distill takes it."""
+        zero_logprob_backward(logits, ids, lse, dlogp, grad, entropy=entropy, dentropy=dentropy,
+                              temperature=temperature, ctl=self.ctl, stream=stream)
+
     def prepare_single_pass(self, grad_chunks, copies, stream=None) -> "PreparedSinglePass":
         """single_pass with its arguments marshalled once: for short steps,
         where the per-call argument checks and pointer tables cost host time
@@ -984,3 +1005,9 @@ from .train import (  # noqa: E402,F401
     ZERO_NORM_MAX_COLS, ZERO_NORM_MAX_PARTS, ZERO_Q8_BLOCK, ZERO_Q8_MAX_LD, q8_empty, q8_shape,
     zero_distill, zero_distill_backward, zero_distill_forward, zero_q8_gemm, zero_q8_quantize,
     zero_q8_quantize_ctl, zero_rmsnorm, zero_rmsnorm_backward, zero_rmsnorm_backward_workspace)
+# The operators of zero_model.h: theirs needs the training operators'.
+from .model import (  # noqa: E402,F401
+    ZERO_EMBED_MAX_TOKENS, ZERO_GELU, ZERO_GELU_TANH, ZERO_LAYERNORM_MAX_COLS,
+    ZERO_LOGPROB_MAX_TOP, ZERO_SILU, zero_act, zero_act_backward, zero_embed, zero_embed_backward,
+    zero_embed_backward_workspace, zero_embed_ctl, zero_layernorm, zero_layernorm_backward,
+    zero_layernorm_backward_workspace, zero_logprob, zero_logprob_backward)

@@ -20,7 +20,10 @@ SOURCES = [os.path.join(CSRC, name) for name in (
     "zero_kernels.hip", "zero_abi.cpp",
     # the training operators (zero_train.h)
     "zero_train_abi.cpp", "zero_norm.hip", "zero_norm_backward.hip", "zero_q8.hip",
-    "zero_q8_gemm.hip", "zero_distill.hip")]
+    "zero_q8_gemm.hip", "zero_distill.hip",
+    # the operators of zero_model.h
+    "zero_model_abi.cpp", "zero_embed.hip", "zero_layernorm.hip", "zero_layernorm_backward.hip",
+    "zero_act.hip", "zero_logprob.hip")]
 TWIN_LIB = os.path.join(HERE, "libzerotwin.so")
 TWIN_SOURCES = [os.path.join(CSRC, "zero_twin.hip")]
 # the device side of the seeded input generators (workloads/), test and

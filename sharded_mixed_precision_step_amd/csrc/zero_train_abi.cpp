@@ -2,102 +2,18 @@
 // errors.  Every argument is checked before anything is enqueued.
 #include <stdint.h>
 
-#include "zero_host.h"
+#include "zero_train_checks.h"
 #include "zero_train_internal.h"
 
 namespace {
 
-using zero::aligned;
+using namespace zero::checks;
 using zero::fail;
 using zero::finite_f;
 using zero::hip_fail;
 using zero::ok;
-using zero::overlap;
 
-constexpr int64_t kMaxGrid = 0x7fffffff;   // workgroups of one call, in one launch or several
 constexpr int64_t kMaxTiles = int64_t{1} << 27;  // a band of eight rows of them fits 32 bits
-constexpr int64_t kMaxBytes = int64_t{1} << 56;
-
-// A strided array of one call: what overlap checks and messages need.
-struct Array {
-    const char* name;
-    const void* p;
-    int64_t bytes;   // first byte to one behind the last
-};
-
-int64_t elem_size(int32_t dtype) { return dtype == ZERO_F32 ? 4 : 2; }
-
-int check_dtype(int32_t dtype, const char* who, const char* name) {
-    if (dtype != ZERO_F32 && dtype != ZERO_F16 && dtype != ZERO_BF16)
-        return fail(ZERO_EINVAL, "%s: %s = %d is no element type", who, name, dtype);
-    return ZERO_OK;
-}
-
-int check_fmt(int32_t fmt, const char* who, const char* name) {
-    if (fmt != ZERO_E4M3 && fmt != ZERO_E5M2)
-        return fail(ZERO_EINVAL, "%s: %s = %d is no 8-bit format", who, name, fmt);
-    return ZERO_OK;
-}
-
-int check_size(int64_t n, const char* who, const char* name) {
-    if (n < 0) return fail(ZERO_EINVAL, "%s: %s = %lld < 0", who, name, static_cast<long long>(n));
-    return ZERO_OK;
-}
-
-// rows x cols elements of `size` bytes, rows ld apart; fills out->bytes.
-int check_array(const void* p, int64_t rows, int64_t cols, int64_t ld, int64_t size,
-                uintptr_t alignment, const char* who, const char* name, Array* out) {
-    *out = Array{name, p, 0};
-    if (ld < cols)
-        return fail(ZERO_EINVAL, "%s: ld of %s = %lld is less than a row's %lld", who, name,
-                    static_cast<long long>(ld), static_cast<long long>(cols));
-    int64_t span = 0;
-    if (rows > 0 && cols > 0 &&
-        (__builtin_mul_overflow(rows - 1, ld, &span) || span > kMaxBytes || cols > kMaxBytes ||
-         (span + cols) > kMaxBytes / size))
-        return fail(ZERO_EINVAL, "%s: %s is too large", who, name);
-    if (rows == 0 || cols == 0) return ZERO_OK;  // nothing is touched
-    if (!p) return fail(ZERO_EINVAL, "%s: %s is NULL", who, name);
-    if (!aligned(p, alignment))
-        return fail(ZERO_EALIGN, "%s: %s is not %d-byte aligned", who, name,
-                    static_cast<int>(alignment));
-    out->bytes = (span + cols) * size;
-    return ZERO_OK;
-}
-
-int check_elements(const void* p, int64_t rows, int64_t cols, int64_t ld, int32_t dtype,
-                   const char* who, const char* name, Array* out) {
-    if (int rc = check_dtype(dtype, who, name)) return rc;
-    const int64_t size = elem_size(dtype);
-    return check_array(p, rows, cols, ld, size, static_cast<uintptr_t>(size), who, name, out);
-}
-
-// One q8 matrix: 8-bit data and scale bytes.
-int check_q8(const void* data, int64_t ld, const uint8_t* scales, int64_t ld_s, int64_t rows,
-             int64_t cols, const char* who, const char* data_name, const char* scale_name,
-             Array* data_out, Array* scale_out) {
-    const int64_t blocks = (cols + 127) / 128;
-    if (ld % 16)
-        return fail(ZERO_EALIGN, "%s: ld of %s is not a multiple of 16", who, data_name);
-    if (ld_s % 4)
-        return fail(ZERO_EALIGN, "%s: ld of %s is not a multiple of 4", who, scale_name);
-    if (int rc = check_array(data, rows, blocks * 128, ld, 1, 16, who, data_name, data_out))
-        return rc;
-    return check_array(scales, rows, (blocks + 3) / 4 * 4, ld_s, 1, 4, who, scale_name, scale_out);
-}
-
-// No output shares a byte with an input or with another output.
-int check_apart(const Array* outs, int n_outs, const Array* ins, int n_ins, const char* who) {
-    for (int o = 0; o < n_outs; ++o) {
-        for (int i = 0; i < n_ins; ++i)
-            if (overlap(outs[o].p, outs[o].bytes, ins[i].p, ins[i].bytes))
-                return fail(ZERO_EINVAL, "%s: %s overlaps %s", who, outs[o].name, ins[i].name);
-        for (int p = o + 1; p < n_outs; ++p)
-            if (overlap(outs[o].p, outs[o].bytes, outs[p].p, outs[p].bytes))
-                return fail(ZERO_EINVAL, "%s: %s overlaps %s", who, outs[o].name, outs[p].name);
-    }
-    return ZERO_OK;
-}
 
 int quantize(const void* const* srcs, int n_srcs, int32_t dtype, int64_t rows, int64_t cols,
              int64_t ld_src, int32_t fmt, void* q, int64_t ld_q, uint8_t* s, int64_t ld_s,
@@ -141,11 +57,6 @@ int quantize(const void* const* srcs, int n_srcs, int32_t dtype, int64_t rows, i
     a.dtype = dtype; a.fmt = fmt;
     const hipError_t e = zero::launch_q8_quantize(a, stream);
     return e == hipSuccess ? ok() : hip_fail(e, who);
-}
-
-int check_ctl(const zero_step_control* d_ctl, const char* who) {
-    if (!aligned(d_ctl, 8)) return fail(ZERO_EALIGN, "%s: d_ctl is not 8-byte aligned", who);
-    return ZERO_OK;
 }
 
 int distill(const zero_distill_inputs* in, zero::DistillMode mode, float loss_scale,
@@ -238,12 +149,6 @@ int check_norm_cols(int64_t cols, const char* who) {
         return fail(ZERO_ERANGE, "%s: cols = %lld is above %d", who, static_cast<long long>(cols),
                     ZERO_NORM_MAX_COLS);
     return ZERO_OK;
-}
-
-// Output `out` is exactly `in`: same first byte, type and row stride.
-bool same_array(const void* out, int32_t out_dtype, int64_t ld_out, const void* in,
-                int32_t in_dtype, int64_t ld_in) {
-    return out && out == in && out_dtype == in_dtype && ld_out == ld_in;
 }
 
 }  // namespace
