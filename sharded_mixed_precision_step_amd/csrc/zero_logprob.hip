@@ -4,12 +4,14 @@
 // Forward: one workgroup per row, which goes by once for the running maximum m,
 // the sum s of e = 2^d and the sum w of e d, d = (z - m) log2(e) / temperature:
 //   lse = m / temperature + ln s,   entropy = ln s - ln 2 * w / s
-// For the alternatives each lane also keeps its own largest logit.  The top-th
-// largest of 256 groups of lanes' maxima is at most the row's top-th largest
-// logit, and few others reach it: a second pass over the row (from registers up
-// to 32,768 elements, else mostly from the caches) collects those, and counting
-// how many come before each, by value and place, orders them.  A row with too many
-// such logits (long ties) has its border found by bisection.
+// For the alternatives, each lane's largest logit of the row's first part goes into
+// 256 groups' maxima: the top-th largest of these is reached by `top` logits at least,
+// and by few others.  Packs of eight whose largest reaches it are noted in LDS as the
+// row goes by, so that it is read once; the top-th largest of many such maxima is a
+// closer border, and only the packs that reach that one are looked into.  Counting how
+// many come before each of their logits, by value and place, orders them.  A row with
+// too many on the border (long ties, or logits that rise along the row) is read again,
+// and its border found by bisection.
 #include "zero_device.h"
 #include "zero_model_internal.h"
 
@@ -67,16 +69,18 @@ __device__ __forceinline__ void add(float& s, float& w, float v, float m, float 
     w = __builtin_fmaf(e, fmaxf(d, kFar), w);
 }
 
-// N packs: one maximum and one rescaling for them all.
+// N packs: one rescaling for them all.  Leaves each pack's maximum in `own`.
 template <int B, int N>
-__device__ __forceinline__ void take(Stat& st, const Raw8<B> (&r)[N], bool bf16, float c) {
+__device__ __forceinline__ void take(Stat& st, const Raw8<B>* r, bool bf16, float c, float* own) {
     float f[N][8];
     float m = st.m;
 #pragma unroll
     for (int u = 0; u < N; ++u) {
         widen8<B>(r[u], bf16, f[u]);
+        own[u] = f[u][0];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) m = fmaxf(m, f[u][k]);
+        for (int k = 1; k < 8; ++k) own[u] = fmaxf(own[u], f[u][k]);
+        m = fmaxf(m, own[u]);
     }
     rescale(st, m, c);
 #pragma unroll
@@ -97,21 +101,22 @@ __device__ __forceinline__ uint32_t order_key(float v) {
 __device__ __forceinline__ float key_value(uint32_t key) {
     return as_float(key ^ (key >> 31 ? 0x80000000u : 0xffffffffu));
 }
-constexpr uint32_t kNoKey = 0x007fffffu;  // -inf's: no alternative
+constexpr int kGroups = 256;      // lane groups with a maximum each
+constexpr int kWide = 160;        // more packs or logits get a closer border first
+constexpr int kCollected = 8 * kWide + 16, kRanked = 256;
 
-constexpr int kGroups = 256;     // lane groups with a maximum each
-constexpr int kCandidates = 512;
-
-// The largest key that at least n of 256 values (four a lane, the same in each
-// wave) reach; 0 if there is none but 0.
-__device__ __forceinline__ uint32_t nth_largest(const uint32_t (&v)[4], int n) {
+// Of the numbers of 16 bits that a wave's lanes hold: the largest that at least `top`
+// of them reach; 0 if none but 0 is.
+template <int N>
+__device__ __forceinline__ uint32_t nth_largest(const uint32_t (&v)[N], int top) {
     uint32_t key = 0;
-    for (int b = 31; b >= 0; --b) {
+    for (int b = 15; b >= 0; --b) {
         const uint32_t up = key | 1u << b;
         int count = 0;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) count += __popcll(__ballot(v[k] >= up));
-        if (count >= n) key = up;
+        for (int i = 0; i < N; ++i)
+            count += __popcll(__ballot(v[i] >= up));
+        if (count >= top) key = up;
     }
     return key;
 }
@@ -123,38 +128,222 @@ struct Row {
     float edge_x;
 };
 
-// Calls f(value, place) for each of the lane's logits.
-template <int B, int T, int R, class F>
-__device__ __forceinline__ void for_each(const Row& row, const Raw8<B>* held, bool bf16, F f) {
-    auto pack = [&](const Raw8<B>& r, int p) {
+// Calls f(value, place) for each of the lane's logits, read again.
+template <int B, int T, class F>
+__device__ __forceinline__ void for_each(const Row& row, bool bf16, F f) {
+#pragma unroll 1
+    for (int p = threadIdx.x; p < row.packs; p += T) {
         float v[8];
-        widen8<B>(r, bf16, v);
+        widen8<B>(load_aligned<B>(row.body + static_cast<int64_t>(p) * 8 * B), bf16, v);
 #pragma unroll
         for (int k = 0; k < 8; ++k) f(v[k], row.head + 8 * p + k);
-    };
-    if constexpr (R > 0) {
-#pragma unroll
-        for (int u = 0; u < R; ++u)
-            if (static_cast<int>(threadIdx.x) + u * T < row.packs) pack(held[u], threadIdx.x + u * T);
-    } else {
-        for (int p = threadIdx.x; p < row.packs; p += T)
-            pack(load_aligned<B>(row.body + static_cast<int64_t>(p) * 8 * B), p);
     }
     if (row.edge >= 0) f(row.edge_x, row.edge);
 }
 
-// T lanes per row; R > 0: the row's body is at most R * T packs, and stays in
-// registers.
-template <int DT, int T, int R, bool TOP>
-__global__ __launch_bounds__(T, 4) void logprob_kernel(const LogprobArgs a, int64_t first) {
+// What the alternatives need in LDS.
+template <int PACKS>
+struct Tops {
+    static constexpr int kPacks = PACKS;
+    uint64_t packs[PACKS];           // the packs noted, as entries of their largest
+    uint64_t collected[kCollected];  // their logits that reach the border
+    uint64_t ranked[kRanked];        // those that reach a closer one
+    float group_max[kGroups];
+    float border;
+    uint32_t n_packs, n, n_ranked;
+    uint32_t reach[2][16];
+};
+
+// Larger entries come first: a value, then the places left over.
+__device__ __forceinline__ uint64_t entry(float v, int place) {
+    return static_cast<uint64_t>(order_key(v)) << 32 | (0xffffffffu - static_cast<uint32_t>(place));
+}
+__device__ __forceinline__ float entry_value(uint64_t e) {
+    return key_value(static_cast<uint32_t>(e >> 32));
+}
+__device__ __forceinline__ int entry_place(uint64_t e) {
+    return static_cast<int>(0xffffffffu - static_cast<uint32_t>(e));
+}
+
+// Adds to a list in LDS; what does not fit is only counted.
+__device__ __forceinline__ void push(uint64_t* list, uint32_t& n, int room, uint64_t e) {
+    const uint32_t at = atomicAdd(&n, 1u);
+    if (at < static_cast<uint32_t>(room)) list[at] = e;
+}
+
+// The value that a key of 16 bits begins with; every finite value for 0, since -inf
+// is no alternative.
+__device__ __forceinline__ float border_value(uint32_t key16) {
+    const float v = key_value(key16 << 16);
+    return key16 <= 0x007fu ? kLowest : v;
+}
+
+// A border that the row's `top` largest reach, from the lanes' maxima.
+template <int T, class Tops>
+__device__ __forceinline__ float first_border(Tops& s, float lane_max, int top) {
+    const int t = threadIdx.x;
+#pragma unroll
+    for (int d = 1; d < T / kGroups; d *= 2) lane_max = fmaxf(lane_max, __shfl_xor(lane_max, d));
+    if (t % (T / kGroups) == 0) s.group_max[t / (T / kGroups)] = lane_max;
+    if (t == 0) s.n_packs = s.n = s.n_ranked = 0;
+    __syncthreads();
+    if (t < 64) {
+        uint32_t v[kGroups / 64];
+#pragma unroll
+        for (int i = 0; i < kGroups / 64; ++i) v[i] = order_key(s.group_max[i * 64 + t]) >> 16;
+        const uint32_t key = nth_largest(v, top);
+        if (t == 0) s.border = border_value(key);
+    }
+    __syncthreads();
+    return s.border;
+}
+
+// A closer one, from a list's first 64 N entries (`top` at least).
+template <int N>
+__device__ __forceinline__ float closer(const uint64_t* list, int n, int top) {
+    const int t = threadIdx.x;
+    uint32_t v[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int at = i * 64 + t;
+        const uint32_t key = static_cast<uint32_t>(list[at < n ? at : 0] >> 48);
+        v[i] = at < n ? key : 0;
+    }
+    return border_value(nth_largest(v, top));
+}
+template <class Tops>
+__device__ __forceinline__ float next_border(Tops& s, const uint64_t* list, int n, int top) {
+    if (threadIdx.x < 64) {
+        const float border = n <= 256 ? closer<4>(list, n, top) : closer<16>(list, n, top);
+        if (threadIdx.x == 0) s.border = border;
+    }
+    __syncthreads();
+    return s.border;
+}
+
+// The entries among which the row's `top` largest logits are, and how many they are.
+// s.packs holds the s.n_packs packs that reach `border`, as far as they fit.
+template <int B, int T, class Tops>
+__device__ __forceinline__ const uint64_t* settle(Tops& s, const Row& row, bool bf16, int top,
+                                                  float border, float largest, int* count) {
+    constexpr int kPacks = Tops::kPacks;
+    const int t = threadIdx.x;
+    int packs = static_cast<int>(s.n_packs < kPacks ? s.n_packs : kPacks);
+    bool many = s.n_packs > kPacks;
+    if (packs > kWide) border = next_border(s, s.packs, packs, top);
+    if (many) {  // once more, from memory
+        if (t == 0) s.n_packs = 0;
+        __syncthreads();
+#pragma unroll 1
+        for (int p = t; p < row.packs; p += T) {
+            float v[8], m;
+            widen8<B>(load_aligned<B>(row.body + static_cast<int64_t>(p) * 8 * B), bf16, v);
+            m = v[0];
+#pragma unroll
+            for (int k = 1; k < 8; ++k) m = fmaxf(m, v[k]);
+            if (m >= border) push(s.packs, s.n_packs, kPacks, entry(m, p));
+        }
+        __syncthreads();
+        many = s.n_packs > kPacks;
+        packs = static_cast<int>(s.n_packs);
+    }
+    if (!many) {
+        for (int j = t; j < packs; j += T) {
+            const uint64_t e = s.packs[j];
+            if (!(entry_value(e) >= border)) continue;
+            const int p = entry_place(e);
+            float v[8];
+            widen8<B>(load_aligned<B>(row.body + static_cast<int64_t>(p) * 8 * B), bf16, v);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (v[k] >= border)
+                    push(s.collected, s.n, kCollected, entry(v[k], row.head + 8 * p + k));
+        }
+        if (row.edge_x >= border) push(s.collected, s.n, kCollected, entry(row.edge_x, row.edge));
+        __syncthreads();
+        const int n = static_cast<int>(s.n);
+        many = n > kCollected;
+        *count = n;
+        if (n <= kWide) return s.collected;
+        if (!many) {
+            border = next_border(s, s.collected, n, top);
+            for (int j = t; j < n; j += T) {
+                const uint64_t e = s.collected[j];
+                if (entry_value(e) >= border) push(s.ranked, s.n_ranked, kRanked, e);
+            }
+            __syncthreads();
+            *count = static_cast<int>(s.n_ranked);
+            many = *count > kRanked;
+            if (!many) return s.ranked;
+        }
+    }
+    // bisection: the least entry of the `top` largest, which reach lo
+    uint64_t lo = entry(border, row.vocab), hi = entry(largest, 0);
+#pragma unroll 1
+    for (int turn = 0; lo < hi; turn ^= 1) {
+        const uint64_t mid = lo + (hi - lo) / 2 + ((hi - lo) & 1);
+        uint32_t reach = 0;
+        for_each<B, T>(row, bf16, [&](float v, int place) { reach += entry(v, place) >= mid; });
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) reach += __shfl_xor(reach, d);
+        if ((t & 63) == 0) s.reach[turn][t / 64] = reach;
+        __syncthreads();
+        reach = 0;
+        for (int w = 0; w < T / 64; ++w) reach += s.reach[turn][w];
+        if (reach >= static_cast<uint32_t>(top)) lo = mid;
+        else hi = mid - 1;
+    }
+    __syncthreads();
+    if (t == 0) s.n_ranked = 0;
+    __syncthreads();
+    for_each<B, T>(row, bf16, [&](float v, int place) {
+        const uint64_t e = entry(v, place);
+        if (e >= lo) push(s.ranked, s.n_ranked, kRanked, e);  // `top` of them
+    });
+    __syncthreads();
+    *count = static_cast<int>(s.n_ranked);
+    return s.ranked;
+}
+
+// Writes those of n entries that fewer than `top` others come before, in order.
+template <int DT, int T>
+__device__ __forceinline__ void put_tops(const uint64_t* entries, int n, const LogprobArgs& a,
+                                         int64_t row_at) {
+    const int t = threadIdx.x;
+    const int64_t out = row_at * a.ld_top;
+    // 2^split neighbouring lanes share an entry's comparisons, up to 16
+    int split = 4;
+    while (split > 0 && n << split > T) --split;
+    const int part = t & ((1 << split) - 1);
+    for (int j0 = 0; j0 < n; j0 += T >> split) {
+        const int j = j0 + (t >> split);
+        const uint64_t e = entries[j < n ? j : 0];
+        int rank = 0;
+#pragma unroll 4
+        for (int k = part; k < n; k += 1 << split) rank += entries[k] > e;
+        for (int d = 1; d < 1 << split; d *= 2) rank += __shfl_xor(rank, d);
+        if (j >= n || part != 0 || rank >= a.top) continue;
+        a.top_index[out + rank] = entry_place(e);
+        store1(a.top_logit, out + rank, DT, entry_value(e));
+    }
+    if (t < a.top && t >= n) {
+        a.top_index[out + t] = -1;
+        store1(a.top_logit, out + t, DT, -__builtin_inff());
+    }
+}
+
+// T lanes per row, which take R packs of eight each at a time; without STREAM that is
+// the whole row.
+template <int DT, int T, int R, bool STREAM, bool TOP>
+__global__ __launch_bounds__(T, 8) void logprob_kernel(const LogprobArgs a, int64_t first) {
     constexpr int B = DT == ZERO_F32 ? 4 : 2;
-    constexpr bool bf16 = DT == ZERO_BF16, kHeld = R > 0;
+    constexpr bool bf16 = DT == ZERO_BF16;
     constexpr int kWaves = T / 64;
     __shared__ Stat row_part[kWaves];
-    __shared__ uint32_t group_max[TOP ? kGroups : 1];
-    __shared__ uint32_t cand_key[TOP ? kCandidates : 1], cand_at[TOP ? kCandidates : 1];
-    __shared__ uint32_t count;
-    __shared__ uint32_t counts[2][kWaves];
+    // of a row that is held, few more than `top` packs reach the first border
+    using Lds = Tops<STREAM ? 2048 : 512>;
+    __shared__ __attribute__((aligned(16))) uint8_t tops[TOP ? sizeof(Lds) : 16];
+    Lds& s = *reinterpret_cast<Lds*>(tops);
     const int t = threadIdx.x, wave = t / 64;
     const int64_t row_at = first + blockIdx.x;
     const int64_t id = !a.ids ? 0
@@ -186,72 +375,61 @@ __global__ __launch_bounds__(T, 4) void logprob_kernel(const LogprobArgs a, int6
     row.edge_x = row.edge >= 0 ? load1(row.x, row.edge, DT) : -__builtin_inff();
     const float at_id = a.logp && id < row.vocab ? load1(row.x, id, DT) : 0.0f;
 
-    Raw8<B> held[kHeld ? R : 1];
-    if constexpr (kHeld) {
-        // places behind the row read as -inf
-        const uint32_t fill = B == 4 ? 0xff800000u : bf16 ? 0xff80ff80u : 0xfc00fc00u;
+    // places behind the row read as -inf
+    const uint32_t fill = B == 4 ? 0xff800000u : bf16 ? 0xff80ff80u : 0xfc00fc00u;
+    auto load = [&](Raw8<B>* r, int p0) {
 #pragma unroll
         for (int u = 0; u < R; ++u) {
-            if (t + u * T < row.packs) {
-                held[u] = load_aligned<B>(row.body + static_cast<int64_t>(t + u * T) * 8 * B);
+            const int p = p0 + u * T + t;
+            if (p < row.packs) {
+                r[u] = load_aligned<B>(row.body + static_cast<int64_t>(p) * 8 * B);
             } else {
 #pragma unroll
-                for (int k = 0; k < B / 2; ++k) held[u].v[k] = u32x4{fill, fill, fill, fill};
+                for (int k = 0; k < B / 2; ++k) r[u].v[k] = u32x4{fill, fill, fill, fill};
             }
         }
-    }
+    };
+    float border = 0.0f, own[R];
+    auto note = [&](int p0) {
+#pragma unroll
+        for (int u = 0; u < R; ++u)
+            if (own[u] >= border)
+                push(s.packs, s.n_packs, Lds::kPacks, entry(own[u], p0 + u * T + t));
+    };
+    Raw8<B> r[R];
+    load(r, 0);
     const float inv_tau = 1.0f / a.tau, c = kLog2e * inv_tau;
     Stat st = {kLowest, 0.0f, 0.0f};
-    float lane_max = -__builtin_inff();
-    auto took = [&](const Raw8<B>& r) {
-        if constexpr (TOP) {
-            float v[8];
-            widen8<B>(r, bf16, v);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) lane_max = fmaxf(lane_max, v[k]);
-        }
-    };
-    if constexpr (kHeld) {
+    if constexpr (STREAM) {
+        take<B, R>(st, r, bf16, c, own);
+    } else {
+        // one at a time: its fp32 values have to fit beside the row
 #pragma unroll
         for (int u = 0; u < R; ++u) {
-            const Raw8<B> r[1] = {held[u]};
-            take(st, r, bf16, c);
-            took(r[0]);
+            take<B, 1>(st, r + u, bf16, c, own + u);
             __builtin_amdgcn_sched_barrier(0);
         }
-    } else {
-        constexpr int kUnroll = 4;
-        int p0 = 0;
-        for (; p0 + kUnroll * T <= row.packs; p0 += kUnroll * T) {
-            Raw8<B> r[kUnroll];
+    }
+    if constexpr (TOP) {
+        float lane_max = row.edge_x;
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u)
-                r[u] = load_aligned<B>(row.body + static_cast<int64_t>(p0 + u * T + t) * 8 * B);
-            take(st, r, bf16, c);
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u) took(r[u]);
-        }
-        for (int p = p0 + t; p < row.packs; p += T) {
-            const Raw8<B> r[1] = {load_aligned<B>(row.body + static_cast<int64_t>(p) * 8 * B)};
-            take(st, r, bf16, c);
-            took(r[0]);
+        for (int u = 0; u < R; ++u) lane_max = fmaxf(lane_max, own[u]);
+        border = first_border<T>(s, lane_max, a.top);
+        note(0);
+    }
+    if constexpr (STREAM) {
+        for (int p0 = R * T; p0 < row.packs; p0 += R * T) {
+            load(r, p0);
+            take<B, R>(st, r, bf16, c, own);
+            if constexpr (TOP) note(p0);
         }
     }
     if (row.edge >= 0) {
         rescale(st, fmaxf(st.m, row.edge_x), c);
         add(st.s, st.w, row.edge_x, st.m, c);
-        lane_max = fmaxf(lane_max, row.edge_x);
     }
     st = lanes_join<64>(st, c);
     if ((t & 63) == 0) row_part[wave] = st;
-    if constexpr (TOP) {
-        float m = lane_max;
-#pragma unroll
-        for (int d = 1; d < T / kGroups; d *= 2) m = fmaxf(m, __shfl_xor(m, d));
-        const uint32_t key = order_key(m);
-        if (t % (T / kGroups) == 0) group_max[t / (T / kGroups)] = key > kNoKey ? key : 0;
-        if (t == 0) count = 0;
-    }
     __syncthreads();
     st = lanes_join<kWaves>(row_part[t % kWaves], c);
     const bool bad = !(st.s > 0.0f) || id >= row.vocab || !(st.m < __builtin_inff());
@@ -262,86 +440,16 @@ __global__ __launch_bounds__(T, 4) void logprob_kernel(const LogprobArgs a, int6
         if (a.logp) a.logp[row_at] = bad ? nan : (at_id - st.m) * inv_tau - log_s;
     }
     if constexpr (TOP) {
-        int32_t* index = a.top_index + row_at * a.ld_top;
-        const int64_t logit = row_at * a.ld_top;
         if (bad) {
             if (t < a.top) {
-                index[t] = 0;
-                store1(a.top_logit, logit + t, DT, __builtin_nanf(""));
+                a.top_index[row_at * a.ld_top + t] = 0;
+                store1(a.top_logit, row_at * a.ld_top + t, DT, __builtin_nanf(""));
             }
             return;
         }
-        uint32_t v[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = group_max[4 * (t & 63) + k];
-        uint32_t border = nth_largest(v, a.top);
-        border = border > kNoKey ? border : kNoKey + 1;
-        auto collect = [&](uint32_t key_from, int at_to) {
-            for_each<B, T, R>(row, held, bf16, [&](float f, int at) {
-                const uint32_t key = order_key(f);
-                if (key > key_from || (key == key_from && at <= at_to)) {
-                    const uint32_t n = atomicAdd(&count, 1u);
-                    if (n < kCandidates) {
-                        cand_key[n] = key;
-                        cand_at[n] = static_cast<uint32_t>(at);
-                    }
-                }
-            });
-            __syncthreads();
-        };
-        collect(border, 0x7fffffff);
-        if (count > kCandidates) {
-            // The border by bisection: the largest key that `top` logits reach,
-            // then the place up to which those on it are taken.
-            int turn = 0;
-            auto reach = [&](uint32_t key_from, int at_to) {
-                uint32_t n = 0;
-                for_each<B, T, R>(row, held, bf16, [&](float f, int at) {
-                    const uint32_t key = order_key(f);
-                    n += key > key_from || (key == key_from && at <= at_to);
-                });
-#pragma unroll
-                for (int d = 1; d < 64; d *= 2) n += __shfl_xor(n, d);
-                if ((t & 63) == 0) counts[turn][wave] = n;
-                __syncthreads();
-                n = 0;
-                for (int w = 0; w < kWaves; ++w) n += counts[turn][w];
-                turn ^= 1;
-                return n;
-            };
-            const uint32_t top = static_cast<uint32_t>(a.top);
-            uint32_t lo = border, hi = order_key(st.m);  // lo is reached by `top`
-            while (lo < hi) {
-                const uint32_t mid = lo + (hi - lo + 1) / 2;
-                if (reach(mid, 0x7fffffff) >= top) lo = mid;
-                else hi = mid - 1;
-            }
-            int from = 0, to = row.vocab - 1;
-            while (from < to) {
-                const int mid = from + (to - from) / 2;
-                if (reach(lo, mid) >= top) to = mid;
-                else from = mid + 1;
-            }
-            __syncthreads();
-            if (t == 0) count = 0;
-            __syncthreads();
-            collect(lo, from);
-        }
-        const int n = static_cast<int>(count);
-        for (int j = t; j < n; j += T) {
-            const uint32_t key = cand_key[j], at = cand_at[j];
-            int rank = 0;
-            for (int k = 0; k < n; ++k)
-                rank += cand_key[k] > key || (cand_key[k] == key && cand_at[k] < at);
-            if (rank < a.top) {
-                index[rank] = static_cast<int32_t>(at);
-                store1(a.top_logit, logit + rank, DT, key_value(key));
-            }
-        }
-        if (t < a.top && t >= n) {
-            index[t] = -1;
-            store1(a.top_logit, logit + t, DT, -__builtin_inff());
-        }
+        int n;
+        const uint64_t* entries = settle<B, T>(s, row, bf16, a.top, border, st.m, &n);
+        put_tops<DT, T>(entries, n, a, row_at);
     }
 }
 
@@ -353,10 +461,13 @@ hipError_t logprob_size(const LogprobArgs& a, hipStream_t stream) {
             return hipGetLastError();
         });
     };
-    if (a.vocab <= 256 * 4 * 8) return run(logprob_kernel<DT, 256, 4, TOP>, 256);
-    if (a.vocab <= 512 * 4 * 8) return run(logprob_kernel<DT, 512, 4, TOP>, 512);
-    if (a.vocab <= 1024 * 4 * 8) return run(logprob_kernel<DT, 1024, 4, TOP>, 1024);
-    return run(logprob_kernel<DT, 1024, 0, TOP>, 1024);
+    if (a.vocab <= 256 * 4 * 8) return run(logprob_kernel<DT, 256, 4, false, TOP>, 256);
+    if (a.vocab <= 512 * 4 * 8) return run(logprob_kernel<DT, 512, 4, false, TOP>, 512);
+    if constexpr (!TOP && DT != ZERO_F32) {
+        if (a.vocab <= 512 * 8 * 8) return run(logprob_kernel<DT, 512, 8, false, TOP>, 512);
+    }
+    if (a.vocab <= 1024 * 4 * 8) return run(logprob_kernel<DT, 1024, 4, false, TOP>, 1024);
+    return run(logprob_kernel<DT, 1024, 4, true, TOP>, 1024);
 }
 
 template <int DT>
