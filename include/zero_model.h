@@ -67,7 +67,7 @@ int zero_embed_ctl(const void* const* tables_fp16, int64_t vocab, int64_t cols, 
                    int32_t y_dtype, int64_t ld_y, const zero_step_control* d_ctl, void* stream);
 
 /* Bytes of workspace zero_embed_backward needs (HOST, synchronous): at most
- * 20 * tokens + (tokens + 64) * cols / 4 + 65536 of them; -1 with an error
+ * 20 * tokens + (tokens + 64) * cols / 2 + 65536 of them; -1 with an error
  * text if the sizes are refused. */
 int64_t zero_embed_backward_workspace(int64_t tokens, int64_t vocab, int64_t cols);
 

@@ -5,7 +5,7 @@
 //
 // Backward: the tokens are sorted by their row of the table (a stable radix sort
 // of 6 bits a pass, so that equal ids keep the tokens' order), and the sorted
-// list is cut into pieces of 32 tokens.  A workgroup adds up a piece's rows in
+// list is cut into pieces of 16 tokens.  A workgroup adds up a piece's rows in
 // registers, run by run; a run that lies in one piece goes straight to its row
 // of the table, one that crosses into others leaves a partial row for each, which
 // a second kernel adds up in order.  So one frequent token is the work of many
@@ -179,15 +179,162 @@ __global__ __launch_bounds__(kLanes) void sort_scatter_kernel(const SortPass a) 
     }
 }
 
+// ---- rows of zeros, and the sort of few tokens beside them ------------------
+
+constexpr int kStartLanes = 1024, kStartWaves = kStartLanes / 64;
+constexpr int kSmallRounds = 16;
+constexpr int64_t kSmall = kStartLanes * kSmallRounds;  // tokens that one workgroup sorts
+
+struct Fill {
+    void* p;
+    int64_t cols, ld;
+    uint32_t rows, slices;     // workgroups to a row; to 2^(10 - shift) rows if 1
+    int32_t dtype, shift;      // 2^shift lanes to a row
+};
+
+// One pack a lane and workgroups in order: HBM takes plain stores best one after
+// another (1 GiB 171 us; 178 to 198 with four packs a lane or workgroups that go on).
+__device__ __forceinline__ void fill_zeros(const Fill& f, int64_t tile) {
+    const float zero[8] = {};
+    int64_t row = 0, c = tile * (8 * kStartLanes) + threadIdx.x * 8;
+    if (f.rows > 1) {
+        const uint32_t t = static_cast<uint32_t>(tile), group = t / f.slices;
+        row = static_cast<int64_t>(group) * (kStartLanes >> f.shift) + (threadIdx.x >> f.shift);
+        c = (static_cast<int64_t>(t - group * f.slices) << f.shift |
+             (threadIdx.x & ((1 << f.shift) - 1))) * 8;
+        if (row >= f.rows) return;
+    }
+    const int64_t left = f.cols - c;
+    store8(f.p, row * f.ld + c, static_cast<int>(left < 8 ? left : 8), f.dtype, zero);
+}
+
+// All passes over up to kSmall tokens by one workgroup, the items in registers
+// during a pass and in LDS between passes.
+__device__ void sort_small(const SortPass& a, int passes, uint32_t* lds) {
+    __shared__ uint32_t bins[kStartWaves][kBins];
+    __shared__ uint32_t waves[kStartWaves];
+    const int t = threadIdx.x, wave = t / 64, lane = t % 64;
+    const int n = static_cast<int>(a.tokens);
+    const int rounds = (n + kStartLanes - 1) / kStartLanes;
+    uint16_t* places = reinterpret_cast<uint16_t*>(lds + rounds * kStartLanes);
+    const int i0 = wave * 64 * rounds + lane;
+    const uint64_t below = (uint64_t{1} << lane) - 1;
+    uint32_t key[kSmallRounds], at[kSmallRounds];
+    uint16_t place[kSmallRounds];
+#pragma unroll
+    for (int r = 0; r < kSmallRounds; ++r) {
+        const int i = i0 + r * 64;
+        place[r] = static_cast<uint16_t>(i);
+        key[r] = r < rounds && i < n ? sort_key(a.ids, i, a.id_bytes, a.vocab) : 0;
+    }
+    for (int pass = 0; pass < passes; ++pass) {
+        const int shift = pass * kDigit;
+        bins[wave][lane] = 0;
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < kSmallRounds; ++r) {
+            if (r >= rounds) continue;
+            const bool live = i0 + r * 64 < n;
+            const uint32_t digit = key[r] >> shift & (kBins - 1);
+            uint64_t peers = __ballot(live);
+#pragma unroll
+            for (int b = 0; b < kDigit; ++b) {
+                const uint64_t set = __ballot(digit >> b & 1);
+                peers &= digit >> b & 1 ? set : ~set;
+            }
+            // the first of them counts them all
+            uint32_t old = 0;
+            if (live && (peers & below) == 0)
+                old = atomicAdd(&bins[wave][digit], static_cast<uint32_t>(__popcll(peers)));
+            old = __shfl(old, peers ? __ffsll(static_cast<long long>(peers)) - 1 : lane);
+            at[r] = old + __popcll(peers & below);
+        }
+        __syncthreads();
+        // thread t: digit t / 16 of wave t % 16; items of lower digits and waves
+        {
+            const uint32_t count = bins[t % kStartWaves][t / kStartWaves];
+            uint32_t scan = count;
+#pragma unroll
+            for (int d = 1; d < 64; d *= 2) {
+                const uint32_t v = __shfl_up(scan, d);
+                scan += lane >= d ? v : 0;
+            }
+            if (lane == 63) waves[wave] = scan;
+            __syncthreads();
+            uint32_t before = 0;
+#pragma unroll
+            for (int w = 0; w < kStartWaves; ++w) before += w < wave ? waves[w] : 0;
+            bins[t % kStartWaves][t / kStartWaves] = before + scan - count;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < kSmallRounds; ++r) {
+            if (r >= rounds || i0 + r * 64 >= n) continue;
+            at[r] += bins[wave][key[r] >> shift & (kBins - 1)];
+            lds[at[r]] = key[r];
+            places[at[r]] = place[r];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < kSmallRounds; ++r) {
+            const int i = i0 + r * 64;
+            if (r >= rounds || i >= n) continue;
+            key[r] = lds[i];
+            place[r] = places[i];
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < kSmallRounds; ++r) {
+        const int i = i0 + r * 64;
+        if (r >= rounds || i >= n) continue;
+        a.keys_out[i] = key[r];
+        a.order_out[i] = place[r];
+    }
+}
+
+// Workgroup 0 sorts, if there are passes; the others fill.
+__global__ __launch_bounds__(kStartLanes) void embed_start_kernel(const SortPass a, int passes,
+                                                                  const Fill f, int64_t first) {
+    extern __shared__ uint32_t sort_lds[];
+    const int64_t block = first + blockIdx.x, sorters = passes > 0;
+    if (block < sorters) sort_small(a, passes, sort_lds);
+    else fill_zeros(f, block - sorters);
+}
+
 // ---- sums ------------------------------------------------------------------
 
-constexpr int kPiece = 32;                // sorted tokens per workgroup
-constexpr int kSumSlice = kLanes * 8;     // columns per workgroup
+constexpr int kPiece = 16;                // sorted tokens in a piece, all under way at once
+constexpr int kAtOnce = 8;                // partial rows under way
 
 struct Sorted {
     const uint32_t *keys, *order;
     float* parts;                         // [2 * pieces][cols]
 };
+
+// A piece's lanes: 2^shift of them, at least a wave, eight columns each.
+struct Lanes {
+    int64_t first;
+    uint32_t slices;
+    int32_t shift;
+};
+struct PieceAt {
+    int64_t piece, c;
+    int n;
+};
+__device__ __forceinline__ PieceAt piece_at(const Lanes& l, int64_t cols) {
+    const int64_t block = l.first + blockIdx.x, group = block / l.slices;
+    PieceAt p;
+    p.piece = group * (kLanes >> l.shift) +
+              __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> l.shift));
+    p.c = ((block - group * l.slices) << l.shift | (threadIdx.x & ((1 << l.shift) - 1))) * 8;
+    const int64_t left = cols - p.c;
+    p.n = static_cast<int>(left < 8 ? left : 8);
+    return p;
+}
+
+__device__ __forceinline__ uint32_t lane_value(uint32_t v, int lane) {
+    return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), lane));
+}
 
 __device__ __forceinline__ void put_row(const EmbedBackwardArgs& a, uint32_t row, int64_t c, int n,
                                         float (&sum)[8]) {
@@ -202,30 +349,41 @@ __device__ __forceinline__ void put_row(const EmbedBackwardArgs& a, uint32_t row
 // A piece's runs.  A run that came in from the piece before leaves its sum as
 // the piece's first partial row, one that only goes on into the next as its
 // second.
+template <int DB>
 __global__ __launch_bounds__(kLanes) void embed_sum_kernel(const EmbedBackwardArgs a,
-                                                           const Sorted s, int64_t first,
-                                                           uint32_t slices) {
-    const int64_t block = first + blockIdx.x;
-    const int64_t piece = block / slices;
-    const int64_t c = (block - piece * slices) * kSumSlice + threadIdx.x * 8;
-    if (c >= a.cols) return;
-    const int n = static_cast<int>(a.cols - c < 8 ? a.cols - c : 8);
-    const int64_t i0 = piece * kPiece;
-    const int64_t end = i0 + kPiece < a.tokens ? i0 + kPiece : a.tokens;
+                                                           const Sorted s, const Lanes l) {
+    const PieceAt p = piece_at(l, a.cols);
+    const int64_t i0 = p.piece * kPiece;
+    if (i0 >= a.tokens) return;
+    const int lane = threadIdx.x % 64;
+    const int count = static_cast<int>(a.tokens - i0 < kPiece ? a.tokens - i0 : kPiece);
     const uint32_t none = static_cast<uint32_t>(a.vocab);
-    uint32_t key = s.keys[i0];
-    bool came = piece > 0 && s.keys[i0 - 1] == key;
+    // lane j: the key before the piece's j-th token, so that lane count has the last
+    // one's and lane count + 1 the next piece's; and the j-th token's place
+    const int64_t at = i0 - 1 + lane;
+    const uint32_t keys = at >= 0 && at < a.tokens && lane < count + 2 ? s.keys[at] : none + 1;
+    const uint32_t order = lane < count ? s.order[i0 + lane] : 0;
+    if (p.n <= 0) return;
+    uint32_t key = lane_value(keys, 1);
+    bool came = lane_value(keys, 0) == key;
     float sum[8] = {};
-    for (int64_t i = i0; i < end && key != none; ++i) {
+    Raw8<DB> r[kPiece];
+#pragma unroll
+    for (int j = 0; j < kPiece; ++j)
+        if (j < count && lane_value(keys, j + 1) != none)
+            r[j] = load8<DB>(a.dy, static_cast<int64_t>(lane_value(order, j)) * a.ld_dy + p.c, p.n);
+#pragma unroll
+    for (int j = 0; j < kPiece; ++j) {
+        if (j >= count || key == none) continue;
         float f[8];
-        load_row8(a.dy, static_cast<int64_t>(s.order[i]) * a.ld_dy + c, n, a.dy_dtype, f);
+        widen8<DB>(r[j], a.dy_dtype == ZERO_BF16, f);
 #pragma unroll
         for (int k = 0; k < 8; ++k) sum[k] += f[k];
-        const uint32_t next = i + 1 < a.tokens ? s.keys[i + 1] : none + 1;
-        if (next == key && i + 1 < end) continue;
+        const uint32_t next = lane_value(keys, j + 2);
+        if (next == key && j + 1 < count) continue;
         if (came || next == key)
-            store8(s.parts, (2 * piece + (came ? 0 : 1)) * a.cols + c, n, ZERO_F32, sum);
-        else put_row(a, key, c, n, sum);
+            store8(s.parts, (2 * p.piece + (came ? 0 : 1)) * a.cols + p.c, p.n, ZERO_F32, sum);
+        else put_row(a, key, p.c, p.n, sum);
 #pragma unroll
         for (int k = 0; k < 8; ++k) sum[k] = 0.0f;
         came = false;
@@ -235,63 +393,46 @@ __global__ __launch_bounds__(kLanes) void embed_sum_kernel(const EmbedBackwardAr
 
 // The runs that go on from a piece in which they began.
 __global__ __launch_bounds__(kLanes) void embed_join_kernel(const EmbedBackwardArgs a,
-                                                            const Sorted s, int64_t first,
-                                                            uint32_t slices) {
-    const int64_t block = first + blockIdx.x;
-    const int64_t piece = block / slices;
-    const int64_t end = (piece + 1) * kPiece;
+                                                            const Sorted s, const Lanes l) {
+    const PieceAt p = piece_at(l, a.cols);
+    const int64_t end = (p.piece + 1) * kPiece;
     if (end >= a.tokens) return;
     const uint32_t key = s.keys[end];
-    const int64_t c = (block - piece * slices) * kSumSlice + threadIdx.x * 8;
-    if (key == static_cast<uint32_t>(a.vocab) || s.keys[end - 1] != key || c >= a.cols) return;
-    if (piece > 0 && s.keys[end - kPiece] == key && s.keys[end - kPiece - 1] == key) return;
-    const int n = static_cast<int>(a.cols - c < 8 ? a.cols - c : 8);
+    if (key == static_cast<uint32_t>(a.vocab) || s.keys[end - 1] != key) return;
+    if (p.piece > 0 && s.keys[end - kPiece] == key && s.keys[end - kPiece - 1] == key) return;
+    const int lane = threadIdx.x % 64;
     float sum[8];
-    load_row8(s.parts, (2 * piece + 1) * a.cols + c, n, ZERO_F32, sum);
-    for (int64_t p = piece + 1; p * kPiece < a.tokens && s.keys[p * kPiece] == key; ++p) {
-        float f[8];
-        load_row8(s.parts, 2 * p * a.cols + c, n, ZERO_F32, f);
+    load_row8(s.parts, (2 * p.piece + 1) * a.cols + p.c, p.n, ZERO_F32, sum);
+    for (int64_t first = p.piece + 1;; first += 64) {
+        // how many of the next 64 pieces the run came into
+        const int64_t i = (first + lane) * kPiece;
+        const uint64_t in = __ballot(i < a.tokens && s.keys[i < a.tokens ? i : 0] == key);
+        const int n = ~in ? __ffsll(static_cast<long long>(~in)) - 1 : 64;
+        for (int j0 = 0; j0 < n; j0 += kAtOnce) {
+            Raw8<4> r[kAtOnce];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) sum[k] += f[k];
+            for (int u = 0; u < kAtOnce; ++u)
+                r[u] = load8<4>(s.parts, 2 * (first + (j0 + u < n ? j0 + u : 0)) * a.cols + p.c,
+                                p.n);
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u) {
+                if (j0 + u >= n) continue;
+                float f[8];
+                widen8<4>(r[u], false, f);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) sum[k] += f[k];
+            }
+        }
+        if (n < 64) break;
     }
-    put_row(a, key, c, n, sum);
-}
-
-// ---- rows without tokens ---------------------------------------------------
-
-constexpr int kZeroRows = 8;              // rows of the table per workgroup
-
-// The first place of the sorted keys that holds `key` or more.
-__device__ __forceinline__ int64_t lower_bound(const uint32_t* keys, int64_t n, uint32_t key) {
-    int64_t lo = 0, hi = n;
-    while (lo < hi) {
-        const int64_t mid = (lo + hi) / 2;
-        if (keys[mid] < key) lo = mid + 1;
-        else hi = mid;
-    }
-    return lo;
-}
-
-__global__ __launch_bounds__(kLanes) void embed_zero_kernel(const EmbedBackwardArgs a,
-                                                            const Sorted s, int64_t first) {
-    __shared__ int64_t at[kZeroRows + 1];
-    const int64_t r0 = (first + blockIdx.x) * kZeroRows;
-    if (threadIdx.x <= kZeroRows)
-        at[threadIdx.x] = a.tokens == 0 ? 0 : lower_bound(s.keys, a.tokens,
-                                                          static_cast<uint32_t>(r0 + threadIdx.x));
-    __syncthreads();
-    const float zero[8] = {};
-    for (int r = 0; r < kZeroRows && r0 + r < a.vocab; ++r) {
-        if (at[r] != at[r + 1]) continue;
-        for (int64_t c = threadIdx.x * 8; c < a.cols; c += kLanes * 8)
-            store8(a.dtable, (r0 + r) * a.ld_dt + c,
-                   static_cast<int>(a.cols - c < 8 ? a.cols - c : 8), a.dt_dtype, zero);
-    }
+    put_row(a, key, p.c, p.n, sum);
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t pieces(int64_t tokens) { return ceil_div(tokens, kPiece); }
 int64_t up16(int64_t n) { return (n + 15) & ~int64_t{15}; }
+int piece_shift(int64_t cols) { return cols <= 512 ? 6 : cols <= 1024 ? 7 : 8; }
+int64_t piece_slices(int64_t cols) { return ceil_div(cols, int64_t{8} << piece_shift(cols)); }
 
 }  // namespace
 
@@ -322,14 +463,56 @@ EmbedWorkspace embed_workspace(int64_t tokens, int64_t cols) {
     return w;
 }
 
-int64_t embed_backward_blocks(int64_t tokens, int64_t vocab, int64_t cols) {
-    const int64_t sum = pieces(tokens) * ceil_div(cols, kSumSlice);
-    const int64_t zero = ceil_div(vocab, kZeroRows);
-    return sum > zero ? sum : zero;
+namespace {
+
+// The zeros' workgroups: of a table whose rows leave no gap, of one with strided rows.
+bool gapless(int64_t vocab, int64_t cols, int64_t ld) { return ld == cols || vocab == 1; }
+int fill_shift(int64_t cols) {
+    int shift = 0;
+    while (shift < 10 && (int64_t{8} << shift) < cols) ++shift;
+    return shift;
 }
+int64_t fill_slices(int64_t cols) { return ceil_div(cols, int64_t{8} << fill_shift(cols)); }
+int64_t fill_tiles(int64_t vocab, int64_t cols, int64_t ld) {
+    if (gapless(vocab, cols, ld)) return ceil_div(vocab * cols, 8 * kStartLanes);
+    return ceil_div(vocab, kStartLanes >> fill_shift(cols)) * fill_slices(cols);
+}
+
+}  // namespace
+
+int64_t embed_backward_blocks(int64_t tokens, int64_t vocab, int64_t cols, int64_t ld_dt) {
+    const int64_t sum = ceil_div(pieces(tokens), kLanes >> piece_shift(cols)) * piece_slices(cols);
+    const int64_t fill = 1 + fill_tiles(vocab, cols, ld_dt);
+    return sum > fill ? sum : fill;
+}
+
+namespace {
+
+// The whole sort of many tokens; the last pass's keys and order.
+hipError_t sort_many(SortPass p, uint32_t* const (&keys)[2], uint32_t* const (&order)[2],
+                     hipStream_t stream, Sorted* s) {
+    const uint32_t grid = static_cast<uint32_t>(ceil_div(p.tokens, kSortItems));
+    int to = 0;
+    for (p.shift = 0; p.vocab >> p.shift; p.shift += kDigit, to ^= 1) {
+        p.keys_out = keys[to];
+        p.order_out = order[to];
+        sort_count_kernel<<<grid, kLanes, 0, stream>>>(p);
+        sort_scatter_kernel<<<grid, kLanes, 0, stream>>>(p);
+        p.keys_in = keys[to];
+        p.order_in = order[to];
+    }
+    s->keys = p.keys_in;
+    s->order = p.order_in;
+    return hipGetLastError();
+}
+
+}  // namespace
 
 hipError_t launch_embed_backward(const EmbedBackwardArgs& a, hipStream_t stream) {
     Sorted s = {};
+    SortPass p = {};
+    int passes = 0;  // of the first launch's own sort
+    size_t lds = 0;
     if (a.tokens > 0) {
         const EmbedWorkspace w = embed_workspace(a.tokens, a.cols);
         uint32_t *keys[2], *order[2];
@@ -337,41 +520,59 @@ hipError_t launch_embed_backward(const EmbedBackwardArgs& a, hipStream_t stream)
             keys[k] = reinterpret_cast<uint32_t*>(a.workspace + w.keys[k]);
             order[k] = reinterpret_cast<uint32_t*>(a.workspace + w.order[k]);
         }
-        SortPass p = {};
         p.ids = a.ids;
         p.counts = reinterpret_cast<uint32_t*>(a.workspace + w.counts);
         p.tokens = a.tokens; p.vocab = a.vocab; p.id_bytes = a.id_bytes;
-        const uint32_t grid = static_cast<uint32_t>(ceil_div(a.tokens, kSortItems));
-        int to = 0;
-        for (p.shift = 0; a.vocab >> p.shift; p.shift += kDigit, to ^= 1) {
-            p.keys_out = keys[to];
-            p.order_out = order[to];
-            sort_count_kernel<<<grid, kLanes, 0, stream>>>(p);
-            sort_scatter_kernel<<<grid, kLanes, 0, stream>>>(p);
-            p.keys_in = keys[to];
-            p.order_in = order[to];
-        }
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-        s.keys = p.keys_in;
-        s.order = p.order_in;
         s.parts = reinterpret_cast<float*>(a.workspace + w.parts);
-        const uint32_t slices = static_cast<uint32_t>(ceil_div(a.cols, kSumSlice));
-        for (int join = 0; join < 2; ++join) {
-            const hipError_t e = in_launches(
-                pieces(a.tokens) * slices, kLanes, [&](int64_t first, uint32_t grid) {
-                    if (join) embed_join_kernel<<<grid, kLanes, 0, stream>>>(a, s, first, slices);
-                    else embed_sum_kernel<<<grid, kLanes, 0, stream>>>(a, s, first, slices);
-                    return hipGetLastError();
-                });
+        if (a.tokens <= kSmall) {
+            while (a.vocab >> (passes * kDigit)) ++passes;
+            lds = static_cast<size_t>(ceil_div(a.tokens, kStartLanes)) * kStartLanes * 6;
+            p.keys_out = keys[0];
+            p.order_out = order[0];
+            s.keys = keys[0];
+            s.order = order[0];
+        } else {
+            const hipError_t e = sort_many(p, keys, order, stream, &s);
             if (e != hipSuccess) return e;
         }
     }
-    if (a.accumulate) return hipSuccess;
-    return in_launches(ceil_div(a.vocab, kZeroRows), kLanes, [&](int64_t first, uint32_t grid) {
-        embed_zero_kernel<<<grid, kLanes, 0, stream>>>(a, s, first);
-        return hipGetLastError();
-    });
+    int64_t tiles = 0;
+    Fill f = {};
+    if (!a.accumulate) {
+        // rows without a gap between them are one long row
+        const bool whole = gapless(a.vocab, a.cols, a.ld_dt);
+        f.p = a.dtable;
+        f.dtype = a.dt_dtype;
+        f.ld = a.ld_dt;
+        f.rows = whole ? 1 : static_cast<uint32_t>(a.vocab);
+        f.cols = whole ? a.vocab * a.cols : a.cols;
+        f.shift = fill_shift(a.cols);
+        f.slices = static_cast<uint32_t>(fill_slices(a.cols));
+        tiles = fill_tiles(a.vocab, a.cols, a.ld_dt);
+    }
+    const hipError_t e = in_launches(
+        tiles + (passes > 0), kStartLanes, [&](int64_t first, uint32_t grid) {
+            embed_start_kernel<<<grid, kStartLanes, lds, stream>>>(p, passes, f, first);
+            return hipGetLastError();
+        });
+    if (e != hipSuccess) return e;
+    if (a.tokens == 0) return hipSuccess;
+    for (int join = 0; join < 2; ++join) {
+        if (join && a.tokens <= kPiece) break;
+        const hipError_t e = in_launches(
+            ceil_div(pieces(a.tokens), kLanes >> piece_shift(a.cols)) * piece_slices(a.cols), kLanes,
+            [&](int64_t first, uint32_t grid) {
+                const Lanes l = {first, static_cast<uint32_t>(piece_slices(a.cols)),
+                                 piece_shift(a.cols)};
+                if (join) embed_join_kernel<<<grid, kLanes, 0, stream>>>(a, s, l);
+                else if (a.dy_dtype == ZERO_F32)
+                    embed_sum_kernel<4><<<grid, kLanes, 0, stream>>>(a, s, l);
+                else embed_sum_kernel<2><<<grid, kLanes, 0, stream>>>(a, s, l);
+                return hipGetLastError();
+            });
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace zero

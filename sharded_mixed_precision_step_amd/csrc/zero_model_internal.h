@@ -38,7 +38,8 @@ struct EmbedBackwardArgs {
     void* dtable;
     char* workspace;               // embed_workspace(tokens, cols).bytes
 };
-int64_t embed_backward_blocks(int64_t tokens, int64_t vocab, int64_t cols);  // the largest launch's
+// Workgroups of the largest of a call's launches.
+int64_t embed_backward_blocks(int64_t tokens, int64_t vocab, int64_t cols, int64_t ld_dt);
 hipError_t launch_embed_backward(const EmbedBackwardArgs& a, hipStream_t stream);
 
 struct LayerNormArgs {

@@ -107,7 +107,7 @@ def test_embed_backward_refuses(kw, code, word):
 @pytest.mark.parametrize("cols", [1, 64, 1001, 4096, 2147483647])
 def test_embed_backward_workspace_is_as_documented(tokens, cols):
     n = zs.zero_embed_backward_workspace(tokens, 1000, cols)
-    assert 0 <= n <= 20 * tokens + (tokens + 64) * cols / 4 + 65536
+    assert 0 <= n <= 20 * tokens + (tokens + 64) * cols / 2 + 65536
 
 
 def test_workspace_queries_refuse():
@@ -148,10 +148,13 @@ def test_layernorm_refuses(kw, code, word):
     _refused(_norm(**kw), code, word)
 
 
+NEED = zs.zero_layernorm_backward_workspace(4, 200)
+
+
 def _norm_back(**kw):
     a = dict(dy=A, dt=1, ldd=200, h=B, ht=0, ldh=200, w=C, wt=1, mean=D, rstd=I, dr=E, drt=1,
              ldr=200, rows=4, cols=200, dx=F, dxt=1, ldx=200, dw=G, db=J, dwt=1, ws=H,
-             nws=8 * 4 * 200)
+             nws=NEED)
     a.update(kw)
     return zs.lib.zero_layernorm_backward(*a.values(), None)
 
@@ -162,7 +165,7 @@ def _norm_back(**kw):
     (dict(dwt=4, dw=None), EINVAL, "db"), (dict(rows=-2), EINVAL, "rows"),
     (dict(cols=0), EINVAL, "cols"), (dict(cols=70000), ERANGE, "65536"),
     (dict(rstd=None), EINVAL, "rstd"), (dict(mean=None), EINVAL, "mean"),
-    (dict(dx=None), EINVAL, "dx"), (dict(ldh=10), EINVAL, "h "), (dict(nws=6399), ERANGE, "6400"),
+    (dict(dx=None), EINVAL, "dx"), (dict(ldh=10), EINVAL, "h "), (dict(nws=NEED - 1), ERANGE, str(NEED)),
     (dict(ws=None), EINVAL, "workspace"), (dict(ws=H + 4), EALIGN, "workspace"),
     (dict(dx=A, ldx=201), EINVAL, "overlaps"), (dict(dx=B), EINVAL, "overlaps"),
     (dict(dx=D), EINVAL, "overlaps"), (dict(dx=I), EINVAL, "overlaps"),
