@@ -33,11 +33,25 @@ __device__ __forceinline__ Slope slope(float g) {
         const Slope p = sigmoid(g);
         return {p.s, p.s * p.d};
     } else if constexpr (KIND == ZERO_GELU) {
-        // Phi by the complementary error function, which keeps its places where
-        // Phi is small; phi(g) = exp(-g^2 / 2) / sqrt(2 pi)
-        constexpr float kRoot = 0.70710678f, kPhi = 0.39894228f;
-        return {0.5f * erfcf(-g * kRoot),
-                kPhi * __builtin_amdgcn_exp2f(-0.5f * kLog2e * g * g)};
+        // With x = |g|: Phi(-x) = exp(-x^2 / 2) t P(t), t = 1 / (1 + x / 4), P a
+        // polynomial fitted to the scaled complementary error function (5e-8 of the
+        // value); Phi(x) = 1 - Phi(-x).  So small values of Phi keep their places, and
+        // the derivative's exponential serves both.  (With the library's complementary
+        // error function: 8192 x 2048 fp16 30 us, 19 with the tanh form.)
+        const float x = fabsf(g), t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.25f, x, 1.0f));
+        const float e = __builtin_amdgcn_exp2f(-0.5f * kLog2e * x * x);
+        float m = 0.019782092f;
+        m = __builtin_fmaf(m, t, -0.080877684f);
+        m = __builtin_fmaf(m, t, 0.09559778f);
+        m = __builtin_fmaf(m, t, -0.031718224f);
+        m = __builtin_fmaf(m, t, 0.063699536f);
+        m = __builtin_fmaf(m, t, 0.058974996f);
+        m = __builtin_fmaf(m, t, 0.08160314f);
+        m = __builtin_fmaf(m, t, 0.09346635f);
+        m = __builtin_fmaf(m, t, 0.09973643f);
+        m = __builtin_fmaf(m, t, 0.099735565f);
+        const float tail = e * t * m;
+        return {g < 0.0f ? tail : 1.0f - tail, 0.39894228f * e};
     } else {
         // (1 + tanh u) / 2 = 1 / (1 + exp(-2u)), u = k (g + 0.044715 g^3); both
         // are 0 or 1 long before 64, and g^3 stays in range
