@@ -309,7 +309,7 @@ __device__ __forceinline__ const uint64_t* settle(Tops& s, const Row& row, bool 
 template <int DT, int T>
 __device__ __forceinline__ void put_tops(const uint64_t* entries, int n, const LogprobArgs& a,
                                          int64_t row_at) {
-    const int t = threadIdx.x;
+    const int t = threadIdx.x & (T - 1);
     const int64_t out = row_at * a.ld_top;
     // 2^split neighbouring lanes share an entry's comparisons, up to 16
     int split = 4;
@@ -326,43 +326,24 @@ __device__ __forceinline__ void put_tops(const uint64_t* entries, int n, const L
         a.top_index[out + rank] = entry_place(e);
         store1(a.top_logit, out + rank, DT, entry_value(e));
     }
-    if (t < a.top && t >= n) {
-        a.top_index[out + t] = -1;
-        store1(a.top_logit, out + t, DT, -__builtin_inff());
+    for (int j = t; j < a.top; j += T) {
+        if (j < n) continue;
+        a.top_index[out + j] = -1;
+        store1(a.top_logit, out + j, DT, -__builtin_inff());
     }
 }
 
-// T lanes per row, which take R packs of eight each at a time; without STREAM that is
-// the whole row.
-template <int DT, int T, int R, bool STREAM, bool TOP>
-__global__ __launch_bounds__(T, 8) void logprob_kernel(const LogprobArgs a, int64_t first) {
+__device__ __forceinline__ int64_t load_id(const void* ids, int64_t row, int bytes) {
+    if (!ids) return 0;
+    return bytes == 8 ? static_cast<const int64_t*>(ids)[row]
+                      : static_cast<int64_t>(static_cast<const int32_t*>(ids)[row]);
+}
+
+// A row as a head up to the first 16-byte border, packs of eight, and a tail; head
+// and tail, at most 14 elements, lie one to a lane t.
+template <int DT>
+__device__ __forceinline__ Row row_of(const LogprobArgs& a, int64_t row_at, int t) {
     constexpr int B = DT == ZERO_F32 ? 4 : 2;
-    constexpr bool bf16 = DT == ZERO_BF16;
-    constexpr int kWaves = T / 64;
-    __shared__ Stat row_part[kWaves];
-    // of a row that is held, few more than `top` packs reach the first border
-    using Lds = Tops<STREAM ? 2048 : 512>;
-    __shared__ __attribute__((aligned(16))) uint8_t tops[TOP ? sizeof(Lds) : 16];
-    Lds& s = *reinterpret_cast<Lds*>(tops);
-    const int t = threadIdx.x, wave = t / 64;
-    const int64_t row_at = first + blockIdx.x;
-    const int64_t id = !a.ids ? 0
-                       : a.id_bytes == 8 ? static_cast<const int64_t*>(a.ids)[row_at]
-                                         : static_cast<const int32_t*>(a.ids)[row_at];
-    if (id < 0) {
-        if (t == 0) {
-            if (a.logp) a.logp[row_at] = 0.0f;
-            if (a.entropy) a.entropy[row_at] = 0.0f;
-            if (a.lse) a.lse[row_at] = 0.0f;
-        }
-        if (TOP && t < a.top) {
-            a.top_index[row_at * a.ld_top + t] = -1;
-            store1(a.top_logit, row_at * a.ld_top + t, DT, -__builtin_inff());
-        }
-        return;
-    }
-    // The row as a head up to the first 16-byte border, packs of eight, and a
-    // tail; head and tail, at most 14 elements, lie one to a lane.
     Row row;
     row.vocab = static_cast<int>(a.vocab);
     row.x = static_cast<const char*>(a.logits) + row_at * a.ld * B;
@@ -373,22 +354,185 @@ __global__ __launch_bounds__(T, 8) void logprob_kernel(const LogprobArgs a, int6
     const int tail = row.head + 8 * row.packs;
     row.edge = t < row.head ? t : t - row.head < row.vocab - tail ? tail + t - row.head : -1;
     row.edge_x = row.edge >= 0 ? load1(row.x, row.edge, DT) : -__builtin_inff();
-    const float at_id = a.logp && id < row.vocab ? load1(row.x, id, DT) : 0.0f;
+    return row;
+}
 
-    // places behind the row read as -inf
-    const uint32_t fill = B == 4 ? 0xff800000u : bf16 ? 0xff80ff80u : 0xfc00fc00u;
-    auto load = [&](Raw8<B>* r, int p0) {
+// The lane's packs p0 + u * T + t; places behind the row read as -inf.
+template <int DT, int T, int R>
+__device__ __forceinline__ void load_packs(const Row& row, int p0, int t,
+                                           Raw8<DT == ZERO_F32 ? 4 : 2>* r) {
+    constexpr int B = DT == ZERO_F32 ? 4 : 2;
+    constexpr uint32_t fill = B == 4 ? 0xff800000u : DT == ZERO_BF16 ? 0xff80ff80u : 0xfc00fc00u;
 #pragma unroll
-        for (int u = 0; u < R; ++u) {
-            const int p = p0 + u * T + t;
-            if (p < row.packs) {
-                r[u] = load_aligned<B>(row.body + static_cast<int64_t>(p) * 8 * B);
-            } else {
+    for (int u = 0; u < R; ++u) {
+        const int p = p0 + u * T + t;
+        if (p < row.packs) {
+            r[u] = load_aligned<B>(row.body + static_cast<int64_t>(p) * 8 * B);
+        } else {
 #pragma unroll
-                for (int k = 0; k < B / 2; ++k) r[u].v[k] = u32x4{fill, fill, fill, fill};
-            }
+            for (int k = 0; k < B / 2; ++k) r[u].v[k] = u32x4{fill, fill, fill, fill};
         }
-    };
+    }
+}
+
+__device__ __forceinline__ void take_edge(Stat& st, const Row& row, float c) {
+    if (row.edge < 0) return;
+    rescale(st, fmaxf(st.m, row.edge_x), c);
+    add(st.s, st.w, row.edge_x, st.m, c);
+}
+
+// The outputs of a row that has no alternatives of its own: left out, or bad.
+template <int DT, int T>
+__device__ __forceinline__ void put_none(const LogprobArgs& a, int64_t row_at, int t, int32_t at,
+                                         float logit) {
+    for (int j = t; j < a.top; j += T) {
+        a.top_index[row_at * a.ld_top + j] = at;
+        store1(a.top_logit, row_at * a.ld_top + j, DT, logit);
+    }
+}
+
+template <int DT, int T, bool TOP>
+__device__ __forceinline__ void put_left_out(const LogprobArgs& a, int64_t row_at, int t) {
+    if (t == 0) {
+        if (a.logp) a.logp[row_at] = 0.0f;
+        if (a.entropy) a.entropy[row_at] = 0.0f;
+        if (a.lse) a.lse[row_at] = 0.0f;
+    }
+    if constexpr (TOP) put_none<DT, T>(a, row_at, t, -1, -__builtin_inff());
+}
+
+// The row's numbers from its statistic; whether it is bad.
+template <int DT, int T, bool TOP>
+__device__ __forceinline__ bool put_row(const LogprobArgs& a, int64_t row_at, int t, const Stat& st,
+                                        int64_t id, float at_id, float inv_tau) {
+    const bool bad = !(st.s > 0.0f) || id >= a.vocab || !(st.m < __builtin_inff());
+    if (t == 0) {
+        const float nan = __builtin_nanf(""), log_s = logf(st.s);
+        if (a.lse) a.lse[row_at] = bad ? nan : __builtin_fmaf(st.m, inv_tau, log_s);
+        if (a.entropy) a.entropy[row_at] = bad ? nan : log_s - kLn2 * (st.w / st.s);
+        if (a.logp) a.logp[row_at] = bad ? nan : (at_id - st.m) * inv_tau - log_s;
+    }
+    if constexpr (TOP) {
+        if (bad) put_none<DT, T>(a, row_at, t, 0, __builtin_nanf(""));
+    }
+    return bad;
+}
+
+// ---- a wave per row ----------------------------------------------------------
+// Rows of up to 2,048 stay in a wave's registers, four packs a lane, and need no
+// barrier.  The top-th largest of the 256 packs' maxima is the border; the logits
+// that reach it take their places in LDS by ballots.
+
+constexpr int kWavePacks = 4, kWaveRows = 4;
+constexpr int kWaveEntries = 512;
+
+template <int DT, bool TOP>
+__global__ __launch_bounds__(64 * kWaveRows, 8) void logprob_wave_kernel(const LogprobArgs a,
+                                                                         int64_t first) {
+    constexpr int B = DT == ZERO_F32 ? 4 : 2, R = kWavePacks;
+    constexpr bool bf16 = DT == ZERO_BF16;
+    __shared__ uint64_t lists[TOP ? kWaveRows : 1][TOP ? kWaveEntries : 1];
+    const int t = threadIdx.x & 63, wave = threadIdx.x / 64;
+    const int64_t row_at = (first + blockIdx.x) * kWaveRows + wave;
+    if (row_at >= a.rows) return;
+    const int64_t id = load_id(a.ids, row_at, a.id_bytes);
+    if (id < 0) {
+        put_left_out<DT, 64, TOP>(a, row_at, t);
+        return;
+    }
+    const Row row = row_of<DT>(a, row_at, t);
+    const float at_id = a.logp && id < row.vocab ? load1(row.x, id, DT) : 0.0f;
+    Raw8<B> r[R];
+    load_packs<DT, 64, R>(row, 0, t, r);
+    const float inv_tau = 1.0f / a.tau, c = kLog2e * inv_tau;
+    Stat st = {kLowest, 0.0f, 0.0f};
+    float own[R];
+#pragma unroll
+    for (int u = 0; u < R; ++u)
+        if (u * 64 < row.packs) take<B, 1>(st, r + u, bf16, c, own + u);
+        else own[u] = -__builtin_inff();
+    take_edge(st, row, c);
+    st = lanes_join<64>(st, c);
+    const bool bad = put_row<DT, 64, TOP>(a, row_at, t, st, id, at_id, inv_tau);
+    if constexpr (TOP) {
+        if (bad) return;
+        uint32_t v[R];
+#pragma unroll
+        for (int u = 0; u < R; ++u) v[u] = order_key(own[u]) >> 16;
+        const float border = border_value(nth_largest(v, a.top));
+        const uint64_t below = (uint64_t{1} << t) - 1;
+        // f(value, place) for each logit of the wave's packs that reach the border, and
+        // of its edges, by whole waves
+        auto each = [&](auto f) {
+#pragma unroll
+            for (int u = 0; u < R; ++u) {
+                if (__ballot(own[u] >= border) == 0) continue;
+                float x[8];
+                widen8<B>(r[u], bf16, x);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) f(x[k], row.head + 8 * (u * 64 + t) + k);
+            }
+            f(row.edge_x, row.edge);
+        };
+        uint64_t* list = lists[wave];
+        int n = 0;
+        auto collect = [&](uint64_t from) {
+            n = 0;
+            each([&](float x, int place) {
+                const uint64_t e = entry(x, place);
+                const uint64_t in = __ballot(x >= border && e >= from);
+                const int at = n + __popcll(in & below);
+                if ((in >> t & 1) && at < kWaveEntries) list[at] = e;
+                n += __popcll(in);
+            });
+        };
+        collect(0);
+        if (n > kWaveEntries) {
+            // bisection: the least entry of the `top` largest, which reach lo
+            uint64_t lo = entry(border, row.vocab), hi = entry(st.m, 0);
+#pragma unroll 1
+            while (lo < hi) {
+                const uint64_t mid = lo + (hi - lo) / 2 + ((hi - lo) & 1);
+                int reach = 0;
+                each([&](float x, int place) {
+                    reach += __popcll(__ballot(x >= border && entry(x, place) >= mid));
+                });
+                if (reach >= a.top) lo = mid;
+                else hi = mid - 1;
+            }
+            collect(lo);
+        }
+        // the wave's writes to its list before its reads of it
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        put_tops<DT, 64>(list, n, a, row_at);
+    }
+}
+
+// ---- a workgroup per row -------------------------------------------------------
+
+// T lanes per row, which take R packs of eight each at a time; without STREAM that is
+// the whole row.
+template <int DT, int T, int R, bool STREAM, bool TOP>
+__global__ __launch_bounds__(T, 8) void logprob_kernel(const LogprobArgs a, int64_t first) {
+    constexpr int B = DT == ZERO_F32 ? 4 : 2;
+    constexpr bool bf16 = DT == ZERO_BF16;
+    constexpr int kWaves = T / 64;
+    // of a row that is held, few more than `top` packs reach the first border
+    using Lds = Tops<STREAM ? 2048 : 512>;
+    __shared__ Stat row_part[kWaves];
+    __shared__ __attribute__((aligned(16))) uint8_t tops[TOP ? sizeof(Lds) : 16];
+    Lds& s = *reinterpret_cast<Lds*>(tops);
+    const int t = threadIdx.x, wave = t / 64;
+    const int64_t row_at = first + blockIdx.x;
+    const int64_t id = load_id(a.ids, row_at, a.id_bytes);
+    if (id < 0) {
+        put_left_out<DT, T, TOP>(a, row_at, t);
+        return;
+    }
+    const Row row = row_of<DT>(a, row_at, t);
+    const float at_id = a.logp && id < row.vocab ? load1(row.x, id, DT) : 0.0f;
     float border = 0.0f, own[R];
     auto note = [&](int p0) {
 #pragma unroll
@@ -397,7 +541,7 @@ __global__ __launch_bounds__(T, 8) void logprob_kernel(const LogprobArgs a, int6
                 push(s.packs, s.n_packs, Lds::kPacks, entry(own[u], p0 + u * T + t));
     };
     Raw8<B> r[R];
-    load(r, 0);
+    load_packs<DT, T, R>(row, 0, t, r);
     const float inv_tau = 1.0f / a.tau, c = kLog2e * inv_tau;
     Stat st = {kLowest, 0.0f, 0.0f};
     if constexpr (STREAM) {
@@ -419,34 +563,19 @@ __global__ __launch_bounds__(T, 8) void logprob_kernel(const LogprobArgs a, int6
     }
     if constexpr (STREAM) {
         for (int p0 = R * T; p0 < row.packs; p0 += R * T) {
-            load(r, p0);
+            load_packs<DT, T, R>(row, p0, t, r);
             take<B, R>(st, r, bf16, c, own);
             if constexpr (TOP) note(p0);
         }
     }
-    if (row.edge >= 0) {
-        rescale(st, fmaxf(st.m, row.edge_x), c);
-        add(st.s, st.w, row.edge_x, st.m, c);
-    }
+    take_edge(st, row, c);
     st = lanes_join<64>(st, c);
     if ((t & 63) == 0) row_part[wave] = st;
     __syncthreads();
     st = lanes_join<kWaves>(row_part[t % kWaves], c);
-    const bool bad = !(st.s > 0.0f) || id >= row.vocab || !(st.m < __builtin_inff());
-    if (t == 0) {
-        const float nan = __builtin_nanf(""), log_s = logf(st.s);
-        if (a.lse) a.lse[row_at] = bad ? nan : __builtin_fmaf(st.m, inv_tau, log_s);
-        if (a.entropy) a.entropy[row_at] = bad ? nan : log_s - kLn2 * (st.w / st.s);
-        if (a.logp) a.logp[row_at] = bad ? nan : (at_id - st.m) * inv_tau - log_s;
-    }
+    const bool bad = put_row<DT, T, TOP>(a, row_at, t, st, id, at_id, inv_tau);
     if constexpr (TOP) {
-        if (bad) {
-            if (t < a.top) {
-                a.top_index[row_at * a.ld_top + t] = 0;
-                store1(a.top_logit, row_at * a.ld_top + t, DT, __builtin_nanf(""));
-            }
-            return;
-        }
+        if (bad) return;
         int n;
         const uint64_t* entries = settle<B, T>(s, row, bf16, a.top, border, st.m, &n);
         put_tops<DT, T>(entries, n, a, row_at);
@@ -461,6 +590,13 @@ hipError_t logprob_size(const LogprobArgs& a, hipStream_t stream) {
             return hipGetLastError();
         });
     };
+    if (a.vocab <= 64 * kWavePacks * 8)
+        return in_launches((a.rows + kWaveRows - 1) / kWaveRows, 64 * kWaveRows,
+                           [&](int64_t first, uint32_t grid) {
+                               logprob_wave_kernel<DT, TOP>
+                                   <<<grid, 64 * kWaveRows, 0, stream>>>(a, first);
+                               return hipGetLastError();
+                           });
     if (a.vocab <= 256 * 4 * 8) return run(logprob_kernel<DT, 256, 4, false, TOP>, 256);
     if (a.vocab <= 512 * 4 * 8) return run(logprob_kernel<DT, 512, 4, false, TOP>, 512);
     if constexpr (!TOP && DT != ZERO_F32) {
@@ -478,20 +614,21 @@ hipError_t logprob_type(const LogprobArgs& a, hipStream_t stream) {
 // ---- gradient --------------------------------------------------------------
 
 constexpr int kGradLanes = 256, kGradPacks = 4;
-constexpr int64_t kGradSlice = int64_t{8} * kGradLanes * kGradPacks;  // logits per workgroup
 
-// p_v and log p_v come from lse, so a row's slices are independent.
-template <int DT>
+// 2^shift lanes to a row, U packs of eight a lane.  p_v and log p_v come from lse, so
+// a row's slices are independent.
+template <int DT, int U>
 __global__ __launch_bounds__(kGradLanes) void logprob_backward_kernel(const LogprobBackwardArgs a,
-                                                                      int64_t first,
+                                                                      int64_t first, int shift,
                                                                       uint32_t slices) {
     constexpr int B = DT == ZERO_F32 ? 4 : 2;
-    const int64_t block = first + blockIdx.x;
-    const int64_t row = block / slices;
-    const int64_t v0 = (block - row * slices) * kGradSlice + threadIdx.x * 8;
-    const int64_t id = !a.ids ? 0
-                       : a.id_bytes == 8 ? static_cast<const int64_t*>(a.ids)[row]
-                                         : static_cast<const int32_t*>(a.ids)[row];
+    const uint32_t block = static_cast<uint32_t>(first + blockIdx.x);  // all of them fit
+    const uint32_t group = block / slices;
+    const int64_t row = static_cast<int64_t>(group) * (kGradLanes >> shift) + (threadIdx.x >> shift);
+    if (row >= a.rows) return;
+    const int64_t v0 = (static_cast<int64_t>(block - group * slices) * U << shift |
+                        (threadIdx.x & ((1 << shift) - 1))) * 8;
+    const int64_t id = load_id(a.ids, row, a.id_bytes);
     const float inv_tau = 1.0f / a.tau, S = a.ctl ? a.ctl->scale : a.S;
     float da = a.dlogp ? a.dlogp[row] : 0.0f, db = a.dentropy ? a.dentropy[row] : 0.0f;
     const bool off = id < 0 || (da == 0.0f && db == 0.0f);
@@ -499,17 +636,17 @@ __global__ __launch_bounds__(kGradLanes) void logprob_backward_kernel(const Logp
     const float entropy = db != 0.0f ? a.entropy[row] : 0.0f;
     da = S * da * inv_tau;
     db = S * db * inv_tau;
-    Raw8<B> r[kGradPacks];
+    Raw8<B> r[U];
     if (!off) {
 #pragma unroll
-        for (int u = 0; u < kGradPacks; ++u) {
-            const int64_t v = v0 + u * kGradLanes * 8, left = a.vocab - v;
+        for (int u = 0; u < U; ++u) {
+            const int64_t v = v0 + (int64_t{8} * u << shift), left = a.vocab - v;
             r[u] = load8<B>(a.logits, row * a.ld + v, static_cast<int>(left < 8 ? left : 8));
         }
     }
 #pragma unroll
-    for (int u = 0; u < kGradPacks; ++u) {
-        const int64_t v = v0 + u * kGradLanes * 8, left = a.vocab - v;
+    for (int u = 0; u < U; ++u) {
+        const int64_t v = v0 + (int64_t{8} * u << shift), left = a.vocab - v;
         float f[8] = {};
         if (!off) {
             widen8<B>(r[u], DT == ZERO_BF16, f);
@@ -527,7 +664,18 @@ __global__ __launch_bounds__(kGradLanes) void logprob_backward_kernel(const Logp
     }
 }
 
-int64_t grad_slices(int64_t vocab) { return (vocab + kGradSlice - 1) / kGradSlice; }
+// Lanes per row, as a power of two: what its packs need, up to a workgroup, with four
+// packs a lane beyond that.
+int grad_shift(int64_t vocab) {
+    int shift = 0;
+    while (shift < 8 && (int64_t{8} << shift) < vocab) ++shift;
+    return shift;
+}
+bool grad_wide(int64_t vocab) { return vocab > 8 * kGradLanes; }
+int64_t grad_slices(int64_t vocab) {
+    const int64_t span = 8 * kGradLanes * kGradPacks;
+    return grad_wide(vocab) ? (vocab + span - 1) / span : 1;
+}
 
 }  // namespace
 
@@ -537,21 +685,30 @@ hipError_t launch_logprob(const LogprobArgs& a, hipStream_t stream) {
     return logprob_type<ZERO_BF16>(a, stream);
 }
 
-int64_t logprob_backward_blocks(int64_t rows, int64_t vocab) { return rows * grad_slices(vocab); }
+int64_t logprob_backward_blocks(int64_t rows, int64_t vocab) {
+    const int64_t per = kGradLanes >> grad_shift(vocab);
+    return (rows + per - 1) / per * grad_slices(vocab);
+}
 
 hipError_t launch_logprob_backward(const LogprobBackwardArgs& a, hipStream_t stream) {
+    const int shift = grad_shift(a.vocab);
     const uint32_t slices = static_cast<uint32_t>(grad_slices(a.vocab));
     auto run = [&](auto kernel) {
         return in_launches(
             logprob_backward_blocks(a.rows, a.vocab), kGradLanes,
             [&](int64_t first, uint32_t grid) {
-                kernel<<<grid, kGradLanes, 0, stream>>>(a, first, slices);
+                kernel<<<grid, kGradLanes, 0, stream>>>(a, first, shift, slices);
                 return hipGetLastError();
             });
     };
-    if (a.dtype == ZERO_F32) return run(logprob_backward_kernel<ZERO_F32>);
-    if (a.dtype == ZERO_F16) return run(logprob_backward_kernel<ZERO_F16>);
-    return run(logprob_backward_kernel<ZERO_BF16>);
+    if (grad_wide(a.vocab)) {
+        if (a.dtype == ZERO_F32) return run(logprob_backward_kernel<ZERO_F32, kGradPacks>);
+        if (a.dtype == ZERO_F16) return run(logprob_backward_kernel<ZERO_F16, kGradPacks>);
+        return run(logprob_backward_kernel<ZERO_BF16, kGradPacks>);
+    }
+    if (a.dtype == ZERO_F32) return run(logprob_backward_kernel<ZERO_F32, 1>);
+    if (a.dtype == ZERO_F16) return run(logprob_backward_kernel<ZERO_F16, 1>);
+    return run(logprob_backward_kernel<ZERO_BF16, 1>);
 }
 
 }  // namespace zero
