@@ -33,28 +33,28 @@ __device__ __forceinline__ void load_row8(const void* p, int64_t i, int n, int d
 
 // ---- forward ---------------------------------------------------------------
 
-constexpr int kSlice = 2 * kLanes * 8;  // columns per workgroup, two packs a lane
-
-template <int TB>
-__global__ __launch_bounds__(kLanes) void embed_kernel(const EmbedArgs a, int64_t first,
+// 2^shift lanes to a token, U packs of eight columns a lane.
+template <int TB, int U>
+__global__ __launch_bounds__(kLanes) void embed_kernel(const EmbedArgs a, int64_t first, int shift,
                                                        uint32_t slices) {
-    const int64_t block = first + blockIdx.x;
-    const int64_t token = block / slices;
-    const int64_t c0 = (block - token * slices) * kSlice + threadIdx.x * 8;
+    const uint32_t block = static_cast<uint32_t>(first + blockIdx.x);  // all of them fit
+    const uint32_t group = block / slices;
+    const int64_t token = static_cast<int64_t>(group) * (kLanes >> shift) + (threadIdx.x >> shift);
+    if (token >= a.tokens) return;
+    const int64_t c0 = (static_cast<int64_t>(block - group * slices) * U << shift |
+                        (threadIdx.x & ((1 << shift) - 1))) * 8;
     const int64_t id = load_id(a.ids, token, a.id_bytes);
     const void* table = a.table[a.ctl ? (a.ctl->cur & 1) : 0];
-    Raw8<TB> r[2];
+    Raw8<TB> r[U];
     const bool live = id >= 0 && id < a.vocab;
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-        const int64_t c = c0 + u * kLanes * 8;
-        const int64_t left = a.cols - c;
+    for (int u = 0; u < U; ++u) {
+        const int64_t c = c0 + (int64_t{8} * u << shift), left = a.cols - c;
         r[u] = load8<TB>(table, id * a.ld_t + c, live ? static_cast<int>(left < 8 ? left : 8) : 0);
     }
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-        const int64_t c = c0 + u * kLanes * 8;
-        const int64_t left = a.cols - c;
+    for (int u = 0; u < U; ++u) {
+        const int64_t c = c0 + (int64_t{8} * u << shift), left = a.cols - c;
         float f[8];
         widen8<TB>(r[u], a.t_dtype == ZERO_BF16, f);
 #pragma unroll
@@ -304,7 +304,6 @@ __global__ __launch_bounds__(kStartLanes) void embed_start_kernel(const SortPass
 // ---- sums ------------------------------------------------------------------
 
 constexpr int kPiece = 16;                // sorted tokens in a piece, all under way at once
-constexpr int kAtOnce = 8;                // partial rows under way
 
 struct Sorted {
     const uint32_t *keys, *order;
@@ -391,41 +390,54 @@ __global__ __launch_bounds__(kLanes) void embed_sum_kernel(const EmbedBackwardAr
     }
 }
 
-// The runs that go on from a piece in which they began.
-__global__ __launch_bounds__(kLanes) void embed_join_kernel(const EmbedBackwardArgs a,
-                                                            const Sorted s, const Lanes l) {
-    const PieceAt p = piece_at(l, a.cols);
-    const int64_t end = (p.piece + 1) * kPiece;
+// The runs that go on from a piece in which they began: 512 columns a workgroup,
+// whose waves take every kJoinWaves-th piece each, added up in the waves' order.
+constexpr int kJoinWaves = 8;
+__global__ __launch_bounds__(64 * kJoinWaves) void embed_join_kernel(const EmbedBackwardArgs a,
+                                                                     const Sorted s, int64_t from,
+                                                                     uint32_t slices) {
+    __shared__ float sums[kJoinWaves][64][8];
+    const int64_t block = from + blockIdx.x, piece = block / slices;
+    const int64_t end = (piece + 1) * kPiece;
     if (end >= a.tokens) return;
     const uint32_t key = s.keys[end];
     if (key == static_cast<uint32_t>(a.vocab) || s.keys[end - 1] != key) return;
-    if (p.piece > 0 && s.keys[end - kPiece] == key && s.keys[end - kPiece - 1] == key) return;
-    const int lane = threadIdx.x % 64;
-    float sum[8];
-    load_row8(s.parts, (2 * p.piece + 1) * a.cols + p.c, p.n, ZERO_F32, sum);
-    for (int64_t first = p.piece + 1;; first += 64) {
+    if (piece > 0 && s.keys[end - kPiece] == key && s.keys[end - kPiece - 1] == key) return;
+    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+    const int64_t c = ((block - piece * slices) * 64 + lane) * 8, left = a.cols - c;
+    const int n = static_cast<int>(left < 8 ? left : 8);
+    float sum[8] = {};
+    if (wave == 0) load_row8(s.parts, (2 * piece + 1) * a.cols + c, n, ZERO_F32, sum);
+    for (int64_t first = piece + 1;; first += 64) {
         // how many of the next 64 pieces the run came into
         const int64_t i = (first + lane) * kPiece;
         const uint64_t in = __ballot(i < a.tokens && s.keys[i < a.tokens ? i : 0] == key);
-        const int n = ~in ? __ffsll(static_cast<long long>(~in)) - 1 : 64;
-        for (int j0 = 0; j0 < n; j0 += kAtOnce) {
-            Raw8<4> r[kAtOnce];
+        const int count = ~in ? __ffsll(static_cast<long long>(~in)) - 1 : 64;
+        Raw8<4> r[64 / kJoinWaves];
 #pragma unroll
-            for (int u = 0; u < kAtOnce; ++u)
-                r[u] = load8<4>(s.parts, 2 * (first + (j0 + u < n ? j0 + u : 0)) * a.cols + p.c,
-                                p.n);
-#pragma unroll
-            for (int u = 0; u < kAtOnce; ++u) {
-                if (j0 + u >= n) continue;
-                float f[8];
-                widen8<4>(r[u], false, f);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) sum[k] += f[k];
-            }
+        for (int u = 0; u < 64 / kJoinWaves; ++u) {
+            const int j = u * kJoinWaves + wave;
+            r[u] = load8<4>(s.parts, 2 * (first + j) * a.cols + c, j < count ? n : 0);
         }
-        if (n < 64) break;
+#pragma unroll
+        for (int u = 0; u < 64 / kJoinWaves; ++u) {
+            float f[8];
+            widen8<4>(r[u], false, f);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) sum[k] += f[k];
+        }
+        if (count < 64) break;
     }
-    put_row(a, key, p.c, p.n, sum);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sums[wave][lane][k] = sum[k];
+    __syncthreads();
+    if (wave != 0) return;
+#pragma unroll
+    for (int w = 1; w < kJoinWaves; ++w) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) sum[k] += sums[w][lane][k];
+    }
+    put_row(a, key, c, n, sum);
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -433,16 +445,34 @@ int64_t pieces(int64_t tokens) { return ceil_div(tokens, kPiece); }
 int64_t up16(int64_t n) { return (n + 15) & ~int64_t{15}; }
 int piece_shift(int64_t cols) { return cols <= 512 ? 6 : cols <= 1024 ? 7 : 8; }
 int64_t piece_slices(int64_t cols) { return ceil_div(cols, int64_t{8} << piece_shift(cols)); }
+int64_t join_slices(int64_t cols) { return ceil_div(cols, 512); }
 
 }  // namespace
 
-int64_t embed_blocks(int64_t tokens, int64_t cols) { return tokens * ceil_div(cols, kSlice); }
+namespace {
+
+// Lanes per token, as a power of two: what its columns need, up to a workgroup, with
+// two packs a lane beyond that.
+int embed_shift(int64_t cols) {
+    int shift = 0;
+    while (shift < 8 && (int64_t{8} << shift) < cols) ++shift;
+    return shift;
+}
+int64_t embed_slices(int64_t cols) { return cols <= 2048 ? 1 : ceil_div(cols, 4096); }
+
+}  // namespace
+
+int64_t embed_blocks(int64_t tokens, int64_t cols) {
+    return ceil_div(tokens, kLanes >> embed_shift(cols)) * embed_slices(cols);
+}
 
 hipError_t launch_embed(const EmbedArgs& a, hipStream_t stream) {
-    const uint32_t slices = static_cast<uint32_t>(ceil_div(a.cols, kSlice));
+    const int shift = embed_shift(a.cols);
+    const uint32_t slices = static_cast<uint32_t>(embed_slices(a.cols));
     return in_launches(embed_blocks(a.tokens, a.cols), kLanes, [&](int64_t first, uint32_t grid) {
-        if (a.t_dtype == ZERO_F32) embed_kernel<4><<<grid, kLanes, 0, stream>>>(a, first, slices);
-        else embed_kernel<2><<<grid, kLanes, 0, stream>>>(a, first, slices);
+        auto run = [&](auto kernel) { kernel<<<grid, kLanes, 0, stream>>>(a, first, shift, slices); };
+        if (a.t_dtype == ZERO_F32) a.cols <= 2048 ? run(embed_kernel<4, 1>) : run(embed_kernel<4, 2>);
+        else a.cols <= 2048 ? run(embed_kernel<2, 1>) : run(embed_kernel<2, 2>);
         return hipGetLastError();
     });
 }
@@ -481,9 +511,9 @@ int64_t fill_tiles(int64_t vocab, int64_t cols, int64_t ld) {
 }  // namespace
 
 int64_t embed_backward_blocks(int64_t tokens, int64_t vocab, int64_t cols, int64_t ld_dt) {
-    const int64_t sum = ceil_div(pieces(tokens), kLanes >> piece_shift(cols)) * piece_slices(cols);
+    const int64_t join = pieces(tokens) * join_slices(cols);  // the sums' are fewer
     const int64_t fill = 1 + fill_tiles(vocab, cols, ld_dt);
-    return sum > fill ? sum : fill;
+    return join > fill ? join : fill;
 }
 
 namespace {
@@ -557,22 +587,23 @@ hipError_t launch_embed_backward(const EmbedBackwardArgs& a, hipStream_t stream)
         });
     if (e != hipSuccess) return e;
     if (a.tokens == 0) return hipSuccess;
-    for (int join = 0; join < 2; ++join) {
-        if (join && a.tokens <= kPiece) break;
-        const hipError_t e = in_launches(
-            ceil_div(pieces(a.tokens), kLanes >> piece_shift(a.cols)) * piece_slices(a.cols), kLanes,
-            [&](int64_t first, uint32_t grid) {
-                const Lanes l = {first, static_cast<uint32_t>(piece_slices(a.cols)),
-                                 piece_shift(a.cols)};
-                if (join) embed_join_kernel<<<grid, kLanes, 0, stream>>>(a, s, l);
-                else if (a.dy_dtype == ZERO_F32)
-                    embed_sum_kernel<4><<<grid, kLanes, 0, stream>>>(a, s, l);
-                else embed_sum_kernel<2><<<grid, kLanes, 0, stream>>>(a, s, l);
-                return hipGetLastError();
-            });
-        if (e != hipSuccess) return e;
-    }
-    return hipSuccess;
+    const int shift = piece_shift(a.cols);
+    const int64_t slices = piece_slices(a.cols), wide = join_slices(a.cols);
+    const hipError_t sum = in_launches(
+        ceil_div(pieces(a.tokens), kLanes >> shift) * slices, kLanes,
+        [&](int64_t first, uint32_t grid) {
+            const Lanes l = {first, static_cast<uint32_t>(slices), shift};
+            if (a.dy_dtype == ZERO_F32) embed_sum_kernel<4><<<grid, kLanes, 0, stream>>>(a, s, l);
+            else embed_sum_kernel<2><<<grid, kLanes, 0, stream>>>(a, s, l);
+            return hipGetLastError();
+        });
+    if (sum != hipSuccess || a.tokens <= kPiece) return sum;
+    return in_launches((pieces(a.tokens) - 1) * wide, 64 * kJoinWaves,
+                       [&](int64_t first, uint32_t grid) {
+                           embed_join_kernel<<<grid, 64 * kJoinWaves, 0, stream>>>(
+                               a, s, first, static_cast<uint32_t>(wide));
+                           return hipGetLastError();
+                       });
 }
 
 }  // namespace zero
