@@ -4,7 +4,7 @@
 // and by HBM for many.
 //
 // Backward: the tokens are sorted by their row of the table (a stable radix sort
-// of 6 bits a pass, so that equal ids keep the tokens' order), and the sorted
+// of 9 bits a pass, so that equal ids keep the tokens' order), and the sorted
 // list is cut into pieces of 16 tokens.  A workgroup adds up a piece's rows in
 // registers, run by run; a run that lies in one piece goes straight to its row
 // of the table, one that crosses into others leaves a partial row for each, which
@@ -66,14 +66,12 @@ __global__ __launch_bounds__(kLanes) void embed_kernel(const EmbedArgs a, int64_
 
 // ---- sort ------------------------------------------------------------------
 
-constexpr int kDigit = 6, kBins = 1 << kDigit;
+constexpr int kDigit = 9, kBins = 1 << kDigit;
 constexpr int kSortRounds = 16;
 constexpr int kSortItems = kLanes * kSortRounds;  // items per workgroup
 
 // A token's key: its row of the table, or vocab (behind all rows) if it has none.
-__device__ __forceinline__ uint32_t sort_key(const void* ids, int64_t i, int bytes,
-                                             int64_t vocab) {
-    const int64_t id = load_id(ids, i, bytes);
+__device__ __forceinline__ uint32_t sort_key(int64_t id, int64_t vocab) {
     return static_cast<uint32_t>(id < 0 || id > vocab ? vocab : id);
 }
 
@@ -81,101 +79,164 @@ struct SortPass {
     const void* ids;            // first pass: the keys come from here
     const uint32_t *keys_in, *order_in;
     uint32_t *keys_out, *order_out, *counts;
+    uint32_t* crossing;         // the list's length, cleared by the first launch
     int64_t tokens, vocab;
     int32_t id_bytes, shift;
 };
 
-__device__ __forceinline__ uint32_t pass_key(const SortPass& a, int64_t i) {
-    return a.keys_in ? a.keys_in[i] : sort_key(a.ids, i, a.id_bytes, a.vocab);
+// The keys of items i0 + r * STEP, all loads under way at once; past the end the
+// last one's.
+template <int N, int STEP>
+__device__ __forceinline__ void load_keys(const SortPass& a, int64_t i0, uint32_t (&key)[N]) {
+    const int64_t last = a.tokens - 1;
+    if (a.keys_in) {
+#pragma unroll
+        for (int r = 0; r < N; ++r) {
+            const int64_t i = i0 + r * STEP;
+            key[r] = a.keys_in[i < last ? i : last];
+        }
+    } else if (a.id_bytes == 8) {
+        int64_t id[N];
+#pragma unroll
+        for (int r = 0; r < N; ++r) {
+            const int64_t i = i0 + r * STEP;
+            id[r] = static_cast<const int64_t*>(a.ids)[i < last ? i : last];
+        }
+#pragma unroll
+        for (int r = 0; r < N; ++r) key[r] = sort_key(id[r], a.vocab);
+    } else {
+        int32_t id[N];
+#pragma unroll
+        for (int r = 0; r < N; ++r) {
+            const int64_t i = i0 + r * STEP;
+            id[r] = static_cast<const int32_t*>(a.ids)[i < last ? i : last];
+        }
+#pragma unroll
+        for (int r = 0; r < N; ++r) key[r] = sort_key(id[r], a.vocab);
+    }
+}
+
+__device__ __forceinline__ void wave_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// A wave's items r * 64 + lane, r < rounds, of which the first `live` exist: how many
+// of its earlier ones have the same digit, in `rank`; and the wave's count of each
+// digit.  The lanes of a round that share a digit find each other by their bits in
+// `peers`; the first of them counts them all and clears the bits.  `peers` and
+// `count` are the wave's own, kBins each, and zero at the start.
+template <int N>
+__device__ __forceinline__ void rank_items(const uint32_t (&key)[N], int shift, int rounds, int live,
+                                           unsigned long long* peers, uint32_t* count,
+                                           uint32_t (&rank)[N]) {
+    const int lane = threadIdx.x & 63;
+    const unsigned long long bit = 1ull << lane;
+#pragma unroll
+    for (int r = 0; r < N; ++r) {
+        if (r >= rounds) continue;
+        const uint32_t digit = key[r] >> shift & (kBins - 1);
+        const bool in = r * 64 + lane < live;
+        if (in) atomicOr(&peers[digit], bit);
+        wave_fence();
+        const unsigned long long same = peers[digit];
+        const uint32_t before = count[digit];
+        wave_fence();
+        rank[r] = before + __popcll(same & (bit - 1));
+        if (in && (same & (bit - 1)) == 0) {
+            count[digit] = before + __popcll(same);
+            peers[digit] = 0;
+        }
+        wave_fence();
+    }
 }
 
 // counts[block][digit]
 __global__ __launch_bounds__(kLanes) void sort_count_kernel(const SortPass a) {
     __shared__ uint32_t bins[kBins];
-    if (threadIdx.x < kBins) bins[threadIdx.x] = 0;
+    for (int d = threadIdx.x; d < kBins; d += kLanes) bins[d] = 0;
+    if (blockIdx.x == 0 && threadIdx.x == 0 && !a.keys_in) *a.crossing = 0;
+    const int64_t i0 = static_cast<int64_t>(blockIdx.x) * kSortItems + threadIdx.x;
+    uint32_t key[kSortRounds];
+    load_keys<kSortRounds, kLanes>(a, i0, key);
     __syncthreads();
-    const int64_t i0 = static_cast<int64_t>(blockIdx.x) * kSortItems;
 #pragma unroll
-    for (int r = 0; r < kSortRounds; ++r) {
-        const int64_t i = i0 + r * kLanes + threadIdx.x;
-        if (i < a.tokens) atomicAdd(&bins[pass_key(a, i) >> a.shift & (kBins - 1)], 1u);
-    }
+    for (int r = 0; r < kSortRounds; ++r)
+        if (i0 + r * kLanes < a.tokens) atomicAdd(&bins[key[r] >> a.shift & (kBins - 1)], 1u);
     __syncthreads();
-    if (threadIdx.x < kBins) a.counts[blockIdx.x * kBins + threadIdx.x] = bins[threadIdx.x];
+    for (int d = threadIdx.x; d < kBins; d += kLanes)
+        a.counts[static_cast<int64_t>(blockIdx.x) * kBins + d] = bins[d];
 }
 
 // Places the items behind those of lower digits, of earlier blocks, waves and
 // rounds, and of lower lanes.
 __global__ __launch_bounds__(kLanes) void sort_scatter_kernel(const SortPass a) {
-    constexpr int kWaves = kLanes / 64;
-    __shared__ uint32_t bins[kWaves][kBins];    // items of a wave so far
-    __shared__ uint32_t sums[2][kWaves][kBins]; // all blocks' and earlier blocks' items
-    __shared__ uint32_t base[kWaves][kBins];
+    constexpr int kWaves = kLanes / 64, kPer = kBins / kLanes;  // digits a lane adds up
+    __shared__ unsigned long long peers[kWaves][kBins];
+    __shared__ uint32_t bins[kWaves][kBins];
+    __shared__ uint32_t waves[kWaves];
     const int t = threadIdx.x, wave = t / 64, lane = t % 64;
-    bins[wave][lane] = 0;
-    uint32_t all = 0, before = 0;
-    for (uint32_t b = wave; b < gridDim.x; b += kWaves) {
-        const uint32_t n = a.counts[b * kBins + lane];
-        all += n;
-        before += b < blockIdx.x ? n : 0;
+    for (int d = t; d < kWaves * kBins; d += kLanes) {
+        peers[0][d] = 0;
+        bins[0][d] = 0;
     }
-    sums[0][wave][lane] = all;
-    sums[1][wave][lane] = before;
-    __syncthreads();
     const int64_t i0 = static_cast<int64_t>(blockIdx.x) * kSortItems + wave * 64 * kSortRounds;
-    const uint64_t below = (uint64_t{1} << lane) - 1;
-    uint32_t key[kSortRounds], rank[kSortRounds];
+    uint32_t key[kSortRounds], rank[kSortRounds], place[kSortRounds];
+    load_keys<kSortRounds, 64>(a, i0 + lane, key);
 #pragma unroll
     for (int r = 0; r < kSortRounds; ++r) {
         const int64_t i = i0 + r * 64 + lane;
-        key[r] = i < a.tokens ? pass_key(a, i) : 0;
+        place[r] = a.order_in ? a.order_in[i < a.tokens ? i : a.tokens - 1]
+                              : static_cast<uint32_t>(i);
     }
+    // digits kPer * t ..: all blocks' items, and the earlier blocks'
+    uint32_t all[kPer] = {}, before[kPer] = {};
+#pragma unroll 8
+    for (uint32_t b = 0; b < gridDim.x; ++b) {
 #pragma unroll
-    for (int r = 0; r < kSortRounds; ++r) {
-        const int64_t i = i0 + r * 64 + lane;
-        const uint32_t digit = key[r] >> a.shift & (kBins - 1);
-        uint64_t peers = __ballot(i < a.tokens);
-#pragma unroll
-        for (int b = 0; b < kDigit; ++b) {
-            const uint64_t set = __ballot(digit >> b & 1);
-            peers &= digit >> b & 1 ? set : ~set;
-        }
-        // the first of them counts them all
-        uint32_t old = 0;
-        if (i < a.tokens && (peers & below) == 0)
-            old = atomicAdd(&bins[wave][digit], static_cast<uint32_t>(__popcll(peers)));
-        old = __shfl(old, peers ? __ffsll(static_cast<long long>(peers)) - 1 : lane);
-        rank[r] = old + __popcll(peers & below);
-    }
-    __syncthreads();
-    if (wave == 0) {
-        uint32_t total = 0, start = 0;
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-            total += sums[0][w][lane];
-            start += sums[1][w][lane];
-        }
-        uint32_t scan = total;
-#pragma unroll
-        for (int d = 1; d < 64; d *= 2) {
-            const uint32_t v = __shfl_up(scan, d);
-            scan += lane >= d ? v : 0;
-        }
-        start += scan - total;
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-            base[w][lane] = start;
-            start += bins[w][lane];
+        for (int k = 0; k < kPer; ++k) {
+            const uint32_t n = a.counts[static_cast<int64_t>(b) * kBins + kPer * t + k];
+            all[k] += n;
+            before[k] += b < blockIdx.x ? n : 0;
         }
     }
     __syncthreads();
+    const int64_t left = a.tokens - i0;
+    rank_items(key, a.shift, kSortRounds, static_cast<int>(left < 0 ? 0 : left < 64 * kSortRounds
+                                                               ? left : 64 * kSortRounds),
+               peers[wave], bins[wave], rank);
+    uint32_t total = 0;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) total += all[k];
+    uint32_t scan = total;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const uint32_t v = __shfl_up(scan, d);
+        scan += lane >= d ? v : 0;
+    }
+    if (lane == 63) waves[wave] = scan;
+    __syncthreads();
+    uint32_t start = scan - total;
+    for (int w = 0; w < wave; ++w) start += waves[w];
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        uint32_t at = start + before[k];
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+            const uint32_t n = bins[w][kPer * t + k];
+            bins[w][kPer * t + k] = at;
+            at += n;
+        }
+        start += all[k];
+    }
+    __syncthreads();
 #pragma unroll
     for (int r = 0; r < kSortRounds; ++r) {
-        const int64_t i = i0 + r * 64 + lane;
-        if (i >= a.tokens) continue;
-        const uint32_t at = base[wave][key[r] >> a.shift & (kBins - 1)] + rank[r];
+        if (i0 + r * 64 + lane >= a.tokens) continue;
+        const uint32_t at = bins[wave][key[r] >> a.shift & (kBins - 1)] + rank[r];
         a.keys_out[at] = key[r];
-        a.order_out[at] = a.order_in ? a.order_in[i] : static_cast<uint32_t>(i);
+        a.order_out[at] = place[r];
     }
 }
 
@@ -209,51 +270,48 @@ __device__ __forceinline__ void fill_zeros(const Fill& f, int64_t tile) {
 }
 
 // All passes over up to kSmall tokens by one workgroup, the items in registers
-// during a pass and in LDS between passes.
+// during a pass and in LDS between passes, where the peers' bits are during one.
+constexpr int kPeersWords = kStartWaves * kBins * 2, kBinsWords = kStartWaves * kBins;
+__host__ __device__ inline int small_words(int rounds) {
+    const int items = rounds * kStartLanes * 6 / 4;
+    return (items > kPeersWords ? items : kPeersWords) + kBinsWords;
+}
 __device__ void sort_small(const SortPass& a, int passes, uint32_t* lds) {
-    __shared__ uint32_t bins[kStartWaves][kBins];
     __shared__ uint32_t waves[kStartWaves];
     const int t = threadIdx.x, wave = t / 64, lane = t % 64;
     const int n = static_cast<int>(a.tokens);
     const int rounds = (n + kStartLanes - 1) / kStartLanes;
+    uint32_t* keys = lds;
     uint16_t* places = reinterpret_cast<uint16_t*>(lds + rounds * kStartLanes);
-    const int i0 = wave * 64 * rounds + lane;
-    const uint64_t below = (uint64_t{1} << lane) - 1;
+    uint32_t* bins = lds + small_words(rounds) - kBinsWords;  // [wave][digit]
+    const int i0 = wave * 64 * rounds + lane, left = n - wave * 64 * rounds;
     uint32_t key[kSmallRounds], at[kSmallRounds];
     uint16_t place[kSmallRounds];
+    if (t == 0) *a.crossing = 0;
+    load_keys<kSmallRounds, 64>(a, i0, key);
 #pragma unroll
-    for (int r = 0; r < kSmallRounds; ++r) {
-        const int i = i0 + r * 64;
-        place[r] = static_cast<uint16_t>(i);
-        key[r] = r < rounds && i < n ? sort_key(a.ids, i, a.id_bytes, a.vocab) : 0;
-    }
+    for (int r = 0; r < kSmallRounds; ++r) place[r] = static_cast<uint16_t>(i0 + r * 64);
     for (int pass = 0; pass < passes; ++pass) {
         const int shift = pass * kDigit;
-        bins[wave][lane] = 0;
+        for (int d = t; d < kPeersWords / 4; d += kStartLanes)
+            reinterpret_cast<u32x4*>(lds)[d] = u32x4{0, 0, 0, 0};
+        for (int d = t; d < kBinsWords / 4; d += kStartLanes)
+            reinterpret_cast<u32x4*>(bins)[d] = u32x4{0, 0, 0, 0};
         __syncthreads();
+        rank_items(key, shift, rounds, left,
+                   reinterpret_cast<unsigned long long*>(lds) + wave * kBins, bins + wave * kBins,
+                   at);
+        __syncthreads();
+        {   // thread t: digit t / 2 of eight waves
+            constexpr int kHalf = kStartWaves / 2;
+            uint32_t* own = bins + (t & 1) * kHalf * kBins + t / 2;
+            uint32_t count[kHalf], total = 0;
 #pragma unroll
-        for (int r = 0; r < kSmallRounds; ++r) {
-            if (r >= rounds) continue;
-            const bool live = i0 + r * 64 < n;
-            const uint32_t digit = key[r] >> shift & (kBins - 1);
-            uint64_t peers = __ballot(live);
-#pragma unroll
-            for (int b = 0; b < kDigit; ++b) {
-                const uint64_t set = __ballot(digit >> b & 1);
-                peers &= digit >> b & 1 ? set : ~set;
+            for (int w = 0; w < kHalf; ++w) {
+                count[w] = own[w * kBins];
+                total += count[w];
             }
-            // the first of them counts them all
-            uint32_t old = 0;
-            if (live && (peers & below) == 0)
-                old = atomicAdd(&bins[wave][digit], static_cast<uint32_t>(__popcll(peers)));
-            old = __shfl(old, peers ? __ffsll(static_cast<long long>(peers)) - 1 : lane);
-            at[r] = old + __popcll(peers & below);
-        }
-        __syncthreads();
-        // thread t: digit t / 16 of wave t % 16; items of lower digits and waves
-        {
-            const uint32_t count = bins[t % kStartWaves][t / kStartWaves];
-            uint32_t scan = count;
+            uint32_t scan = total;
 #pragma unroll
             for (int d = 1; d < 64; d *= 2) {
                 const uint32_t v = __shfl_up(scan, d);
@@ -261,41 +319,46 @@ __device__ void sort_small(const SortPass& a, int passes, uint32_t* lds) {
             }
             if (lane == 63) waves[wave] = scan;
             __syncthreads();
-            uint32_t before = 0;
+            uint32_t start = scan - total;
 #pragma unroll
-            for (int w = 0; w < kStartWaves; ++w) before += w < wave ? waves[w] : 0;
-            bins[t % kStartWaves][t / kStartWaves] = before + scan - count;
+            for (int w = 0; w < kStartWaves; ++w) start += w < wave ? waves[w] : 0;
+#pragma unroll
+            for (int w = 0; w < kHalf; ++w) {
+                own[w * kBins] = start;
+                start += count[w];
+            }
         }
         __syncthreads();
+        const bool last = pass == passes - 1;
 #pragma unroll
         for (int r = 0; r < kSmallRounds; ++r) {
             if (r >= rounds || i0 + r * 64 >= n) continue;
-            at[r] += bins[wave][key[r] >> shift & (kBins - 1)];
-            lds[at[r]] = key[r];
-            places[at[r]] = place[r];
+            at[r] += bins[wave * kBins + (key[r] >> shift & (kBins - 1))];
+            if (last) {
+                a.keys_out[at[r]] = key[r];
+                a.order_out[at[r]] = place[r];
+            } else {
+                keys[at[r]] = key[r];
+                places[at[r]] = place[r];
+            }
         }
+        if (last) return;
         __syncthreads();
 #pragma unroll
         for (int r = 0; r < kSmallRounds; ++r) {
             const int i = i0 + r * 64;
             if (r >= rounds || i >= n) continue;
-            key[r] = lds[i];
+            key[r] = keys[i];
             place[r] = places[i];
         }
-    }
-#pragma unroll
-    for (int r = 0; r < kSmallRounds; ++r) {
-        const int i = i0 + r * 64;
-        if (r >= rounds || i >= n) continue;
-        a.keys_out[i] = key[r];
-        a.order_out[i] = place[r];
+        __syncthreads();  // before the peers' bits take their room
     }
 }
 
 // Workgroup 0 sorts, if there are passes; the others fill.
 __global__ __launch_bounds__(kStartLanes) void embed_start_kernel(const SortPass a, int passes,
                                                                   const Fill f, int64_t first) {
-    extern __shared__ uint32_t sort_lds[];
+    extern __shared__ __attribute__((aligned(16))) uint32_t sort_lds[];
     const int64_t block = first + blockIdx.x, sorters = passes > 0;
     if (block < sorters) sort_small(a, passes, sort_lds);
     else fill_zeros(f, block - sorters);
@@ -308,6 +371,7 @@ constexpr int kPiece = 16;                // sorted tokens in a piece, all under
 struct Sorted {
     const uint32_t *keys, *order;
     float* parts;                         // [2 * pieces][cols]
+    uint32_t *crossing, *list;            // pieces in which a run begins that goes on
 };
 
 // A piece's lanes: 2^shift of them, at least a wave, eight columns each.
@@ -335,20 +399,26 @@ __device__ __forceinline__ uint32_t lane_value(uint32_t v, int lane) {
     return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), lane));
 }
 
+template <int TB>
+__device__ __forceinline__ Raw8<TB> old_row(const EmbedBackwardArgs& a, uint32_t row, int64_t c,
+                                            int n) {
+    return load8<TB>(a.dtable, static_cast<int64_t>(row) * a.ld_dt + c, n);
+}
+// TB > 0: added to `old`, the row's elements of TB bytes.
+template <int TB>
 __device__ __forceinline__ void put_row(const EmbedBackwardArgs& a, uint32_t row, int64_t c, int n,
-                                        float (&sum)[8]) {
-    const int64_t at = static_cast<int64_t>(row) * a.ld_dt + c;
-    float old[8] = {};
-    if (a.accumulate) load_row8(a.dtable, at, n, a.dt_dtype, old);
+                                        const Raw8<TB == 0 ? 2 : TB>& old, float (&sum)[8]) {
+    float f[8] = {};
+    if constexpr (TB != 0) widen8<TB>(old, a.dt_dtype == ZERO_BF16, f);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) sum[k] = old[k] + sum[k] * a.scale;
-    store8(a.dtable, at, n, a.dt_dtype, sum);
+    for (int k = 0; k < 8; ++k) sum[k] = f[k] + sum[k] * a.scale;
+    store8(a.dtable, static_cast<int64_t>(row) * a.ld_dt + c, n, a.dt_dtype, sum);
 }
 
 // A piece's runs.  A run that came in from the piece before leaves its sum as
 // the piece's first partial row, one that only goes on into the next as its
-// second.
-template <int DB>
+// second.  TB > 0: sums are added to the table's rows, which are loaded with dy's.
+template <int DB, int TB>
 __global__ __launch_bounds__(kLanes) void embed_sum_kernel(const EmbedBackwardArgs a,
                                                            const Sorted s, const Lanes l) {
     const PieceAt p = piece_at(l, a.cols);
@@ -367,10 +437,15 @@ __global__ __launch_bounds__(kLanes) void embed_sum_kernel(const EmbedBackwardAr
     bool came = lane_value(keys, 0) == key;
     float sum[8] = {};
     Raw8<DB> r[kPiece];
+    Raw8<TB == 0 ? 2 : TB> old[TB == 0 ? 1 : kPiece];
 #pragma unroll
-    for (int j = 0; j < kPiece; ++j)
-        if (j < count && lane_value(keys, j + 1) != none)
-            r[j] = load8<DB>(a.dy, static_cast<int64_t>(lane_value(order, j)) * a.ld_dy + p.c, p.n);
+    for (int j = 0; j < kPiece; ++j) {
+        const uint32_t own = lane_value(keys, j + 1);
+        if (j >= count || own == none) continue;
+        r[j] = load8<DB>(a.dy, static_cast<int64_t>(lane_value(order, j)) * a.ld_dy + p.c, p.n);
+        if constexpr (TB != 0)
+            if (lane_value(keys, j + 2) != own) old[j] = old_row<TB>(a, own, p.c, p.n);
+    }
 #pragma unroll
     for (int j = 0; j < kPiece; ++j) {
         if (j >= count || key == none) continue;
@@ -380,9 +455,13 @@ __global__ __launch_bounds__(kLanes) void embed_sum_kernel(const EmbedBackwardAr
         for (int k = 0; k < 8; ++k) sum[k] += f[k];
         const uint32_t next = lane_value(keys, j + 2);
         if (next == key && j + 1 < count) continue;
-        if (came || next == key)
+        if (came || next == key) {
             store8(s.parts, (2 * p.piece + (came ? 0 : 1)) * a.cols + p.c, p.n, ZERO_F32, sum);
-        else put_row(a, key, p.c, p.n, sum);
+            if (!came && p.c == 0)
+                s.list[atomicAdd(s.crossing, 1u)] = static_cast<uint32_t>(p.piece);
+        } else {
+            put_row<TB>(a, key, p.c, p.n, old[TB == 0 ? 0 : j], sum);
+        }
 #pragma unroll
         for (int k = 0; k < 8; ++k) sum[k] = 0.0f;
         came = false;
@@ -391,53 +470,64 @@ __global__ __launch_bounds__(kLanes) void embed_sum_kernel(const EmbedBackwardAr
 }
 
 // The runs that go on from a piece in which they began: 512 columns a workgroup,
-// whose waves take every kJoinWaves-th piece each, added up in the waves' order.
-constexpr int kJoinWaves = 8;
+// whose waves take every kJoinWaves-th piece each, added up in the waves' order.  The
+// list's order is chance, each run's sum is not.
+constexpr int kJoinWaves = 8, kJoinBlocks = 512;
+template <int TB>
 __global__ __launch_bounds__(64 * kJoinWaves) void embed_join_kernel(const EmbedBackwardArgs a,
-                                                                     const Sorted s, int64_t from,
+                                                                     const Sorted s,
                                                                      uint32_t slices) {
     __shared__ float sums[kJoinWaves][64][8];
-    const int64_t block = from + blockIdx.x, piece = block / slices;
-    const int64_t end = (piece + 1) * kPiece;
-    if (end >= a.tokens) return;
-    const uint32_t key = s.keys[end];
-    if (key == static_cast<uint32_t>(a.vocab) || s.keys[end - 1] != key) return;
-    if (piece > 0 && s.keys[end - kPiece] == key && s.keys[end - kPiece - 1] == key) return;
     const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-    const int64_t c = ((block - piece * slices) * 64 + lane) * 8, left = a.cols - c;
-    const int n = static_cast<int>(left < 8 ? left : 8);
-    float sum[8] = {};
-    if (wave == 0) load_row8(s.parts, (2 * piece + 1) * a.cols + c, n, ZERO_F32, sum);
-    for (int64_t first = piece + 1;; first += 64) {
-        // how many of the next 64 pieces the run came into
-        const int64_t i = (first + lane) * kPiece;
-        const uint64_t in = __ballot(i < a.tokens && s.keys[i < a.tokens ? i : 0] == key);
-        const int count = ~in ? __ffsll(static_cast<long long>(~in)) - 1 : 64;
-        Raw8<4> r[64 / kJoinWaves];
+    const uint32_t runs = *s.crossing;
+    const uint64_t jobs = static_cast<uint64_t>(runs) * slices;
+    for (uint64_t job = blockIdx.x; job < jobs; job += gridDim.x) {
+        const uint32_t run = static_cast<uint32_t>(job / slices);
+        const int64_t piece = s.list[run];
+        const uint32_t key = s.keys[(piece + 1) * kPiece];
+        const int64_t c = (static_cast<int64_t>(job - static_cast<uint64_t>(run) * slices) * 64 +
+                           lane) * 8;
+        const int64_t left = a.cols - c;
+        const int n = static_cast<int>(left < 8 ? left : 8);
+        float sum[8] = {};
+        Raw8<TB == 0 ? 2 : TB> old;
+        if (wave == 0) {
+            if constexpr (TB != 0) old = old_row<TB>(a, key, c, n);
+            load_row8(s.parts, (2 * piece + 1) * a.cols + c, n, ZERO_F32, sum);
+        }
+        for (int64_t first = piece + 1;; first += 64) {
+            // how many of the next 64 pieces the run came into
+            const int64_t i = (first + lane) * kPiece;
+            const uint64_t in = __ballot(i < a.tokens && s.keys[i < a.tokens ? i : 0] == key);
+            const int count = ~in ? __ffsll(static_cast<long long>(~in)) - 1 : 64;
+            Raw8<4> r[64 / kJoinWaves];
 #pragma unroll
-        for (int u = 0; u < 64 / kJoinWaves; ++u) {
-            const int j = u * kJoinWaves + wave;
-            r[u] = load8<4>(s.parts, 2 * (first + j) * a.cols + c, j < count ? n : 0);
+            for (int u = 0; u < 64 / kJoinWaves; ++u) {
+                const int j = u * kJoinWaves + wave;
+                r[u] = load8<4>(s.parts, 2 * (first + j) * a.cols + c, j < count ? n : 0);
+            }
+#pragma unroll
+            for (int u = 0; u < 64 / kJoinWaves; ++u) {
+                float f[8];
+                widen8<4>(r[u], false, f);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) sum[k] += f[k];
+            }
+            if (count < 64) break;
         }
 #pragma unroll
-        for (int u = 0; u < 64 / kJoinWaves; ++u) {
-            float f[8];
-            widen8<4>(r[u], false, f);
+        for (int k = 0; k < 8; ++k) sums[wave][lane][k] = sum[k];
+        __syncthreads();
+        if (wave == 0) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) sum[k] += f[k];
+            for (int w = 1; w < kJoinWaves; ++w) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) sum[k] += sums[w][lane][k];
+            }
+            put_row<TB>(a, key, c, n, old, sum);
         }
-        if (count < 64) break;
+        __syncthreads();  // before the next job's sums
     }
-#pragma unroll
-    for (int k = 0; k < 8; ++k) sums[wave][lane][k] = sum[k];
-    __syncthreads();
-    if (wave != 0) return;
-#pragma unroll
-    for (int w = 1; w < kJoinWaves; ++w) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) sum[k] += sums[w][lane][k];
-    }
-    put_row(a, key, c, n, sum);
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -488,6 +578,8 @@ EmbedWorkspace embed_workspace(int64_t tokens, int64_t cols) {
     }
     w.counts = at;
     at = up16(at + 4 * kBins * ceil_div(tokens, kSortItems));
+    w.list = at;
+    at = up16(at + 4 * (1 + pieces(tokens)));
     w.parts = at;
     w.bytes = at + 4 * 2 * pieces(tokens) * cols;
     return w;
@@ -511,9 +603,9 @@ int64_t fill_tiles(int64_t vocab, int64_t cols, int64_t ld) {
 }  // namespace
 
 int64_t embed_backward_blocks(int64_t tokens, int64_t vocab, int64_t cols, int64_t ld_dt) {
-    const int64_t join = pieces(tokens) * join_slices(cols);  // the sums' are fewer
+    const int64_t sum = ceil_div(pieces(tokens), kLanes >> piece_shift(cols)) * piece_slices(cols);
     const int64_t fill = 1 + fill_tiles(vocab, cols, ld_dt);
-    return join > fill ? join : fill;
+    return sum > fill ? sum : fill;
 }
 
 namespace {
@@ -536,6 +628,26 @@ hipError_t sort_many(SortPass p, uint32_t* const (&keys)[2], uint32_t* const (&o
     return hipGetLastError();
 }
 
+template <int TB>
+hipError_t sum_and_join(const EmbedBackwardArgs& a, const Sorted& s, hipStream_t stream) {
+    const int shift = piece_shift(a.cols);
+    const int64_t slices = piece_slices(a.cols), wide = join_slices(a.cols);
+    const hipError_t e = in_launches(
+        ceil_div(pieces(a.tokens), kLanes >> shift) * slices, kLanes,
+        [&](int64_t first, uint32_t grid) {
+            const Lanes l = {first, static_cast<uint32_t>(slices), shift};
+            if (a.dy_dtype == ZERO_F32)
+                embed_sum_kernel<4, TB><<<grid, kLanes, 0, stream>>>(a, s, l);
+            else embed_sum_kernel<2, TB><<<grid, kLanes, 0, stream>>>(a, s, l);
+            return hipGetLastError();
+        });
+    if (e != hipSuccess || a.tokens <= kPiece) return e;
+    const int64_t jobs = (pieces(a.tokens) - 1) * wide;
+    embed_join_kernel<TB><<<static_cast<uint32_t>(jobs < kJoinBlocks ? jobs : kJoinBlocks),
+                            64 * kJoinWaves, 0, stream>>>(a, s, static_cast<uint32_t>(wide));
+    return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_embed_backward(const EmbedBackwardArgs& a, hipStream_t stream) {
@@ -552,11 +664,15 @@ hipError_t launch_embed_backward(const EmbedBackwardArgs& a, hipStream_t stream)
         }
         p.ids = a.ids;
         p.counts = reinterpret_cast<uint32_t*>(a.workspace + w.counts);
+        p.crossing = reinterpret_cast<uint32_t*>(a.workspace + w.list);
+        s.crossing = p.crossing;
+        s.list = p.crossing + 1;
         p.tokens = a.tokens; p.vocab = a.vocab; p.id_bytes = a.id_bytes;
         s.parts = reinterpret_cast<float*>(a.workspace + w.parts);
         if (a.tokens <= kSmall) {
             while (a.vocab >> (passes * kDigit)) ++passes;
-            lds = static_cast<size_t>(ceil_div(a.tokens, kStartLanes)) * kStartLanes * 6;
+            lds = 4 * static_cast<size_t>(
+                          small_words(static_cast<int>(ceil_div(a.tokens, kStartLanes))));
             p.keys_out = keys[0];
             p.order_out = order[0];
             s.keys = keys[0];
@@ -587,23 +703,8 @@ hipError_t launch_embed_backward(const EmbedBackwardArgs& a, hipStream_t stream)
         });
     if (e != hipSuccess) return e;
     if (a.tokens == 0) return hipSuccess;
-    const int shift = piece_shift(a.cols);
-    const int64_t slices = piece_slices(a.cols), wide = join_slices(a.cols);
-    const hipError_t sum = in_launches(
-        ceil_div(pieces(a.tokens), kLanes >> shift) * slices, kLanes,
-        [&](int64_t first, uint32_t grid) {
-            const Lanes l = {first, static_cast<uint32_t>(slices), shift};
-            if (a.dy_dtype == ZERO_F32) embed_sum_kernel<4><<<grid, kLanes, 0, stream>>>(a, s, l);
-            else embed_sum_kernel<2><<<grid, kLanes, 0, stream>>>(a, s, l);
-            return hipGetLastError();
-        });
-    if (sum != hipSuccess || a.tokens <= kPiece) return sum;
-    return in_launches((pieces(a.tokens) - 1) * wide, 64 * kJoinWaves,
-                       [&](int64_t first, uint32_t grid) {
-                           embed_join_kernel<<<grid, 64 * kJoinWaves, 0, stream>>>(
-                               a, s, first, static_cast<uint32_t>(wide));
-                           return hipGetLastError();
-                       });
+    if (!a.accumulate) return sum_and_join<0>(a, s, stream);
+    return a.dt_dtype == ZERO_F32 ? sum_and_join<4>(a, s, stream) : sum_and_join<2>(a, s, stream);
 }
 
 }  // namespace zero
