@@ -5,7 +5,8 @@
 //
 // Backward: the tokens are sorted by their row of the table (a stable radix sort
 // of 9 bits a pass, so that equal ids keep the tokens' order), and the sorted
-// list is cut into pieces of 16 tokens.  A workgroup adds up a piece's rows in
+// list is cut into pieces of 16 tokens, or more where there are very many.  A
+// workgroup adds up a piece's rows in
 // registers, run by run; a run that lies in one piece goes straight to its row
 // of the table, one that crosses into others leaves a partial row for each, which
 // a second kernel adds up in order.  So one frequent token is the work of many
@@ -366,12 +367,13 @@ __global__ __launch_bounds__(kStartLanes) void embed_start_kernel(const SortPass
 
 // ---- sums ------------------------------------------------------------------
 
-constexpr int kPiece = 16;                // sorted tokens in a piece, all under way at once
+constexpr int kPiece = 16;                // sorted tokens whose rows are under way at once
 
 struct Sorted {
     const uint32_t *keys, *order;
     float* parts;                         // [2 * pieces][cols]
     uint32_t *crossing, *list;            // pieces in which a run begins that goes on
+    int64_t length;                       // tokens in a piece, a multiple of kPiece
 };
 
 // A piece's lanes: 2^shift of them, at least a wave, eight columns each.
@@ -418,54 +420,61 @@ __device__ __forceinline__ void put_row(const EmbedBackwardArgs& a, uint32_t row
 // A piece's runs.  A run that came in from the piece before leaves its sum as
 // the piece's first partial row, one that only goes on into the next as its
 // second.  TB > 0: sums are added to the table's rows, which are loaded with dy's.
-template <int DB, int TB>
+// LONG: pieces of more than kPiece tokens.
+template <int DB, int TB, bool LONG>
 __global__ __launch_bounds__(kLanes) void embed_sum_kernel(const EmbedBackwardArgs a,
                                                            const Sorted s, const Lanes l) {
     const PieceAt p = piece_at(l, a.cols);
-    const int64_t i0 = p.piece * kPiece;
-    if (i0 >= a.tokens) return;
+    const int64_t length = LONG ? s.length : kPiece, first = p.piece * length;
+    if (first >= a.tokens) return;
+    const int64_t end = first + length < a.tokens ? first + length : a.tokens;
     const int lane = threadIdx.x % 64;
-    const int count = static_cast<int>(a.tokens - i0 < kPiece ? a.tokens - i0 : kPiece);
     const uint32_t none = static_cast<uint32_t>(a.vocab);
-    // lane j: the key before the piece's j-th token, so that lane count has the last
-    // one's and lane count + 1 the next piece's; and the j-th token's place
-    const int64_t at = i0 - 1 + lane;
-    const uint32_t keys = at >= 0 && at < a.tokens && lane < count + 2 ? s.keys[at] : none + 1;
-    const uint32_t order = lane < count ? s.order[i0 + lane] : 0;
-    if (p.n <= 0) return;
-    uint32_t key = lane_value(keys, 1);
-    bool came = lane_value(keys, 0) == key;
     float sum[8] = {};
-    Raw8<DB> r[kPiece];
-    Raw8<TB == 0 ? 2 : TB> old[TB == 0 ? 1 : kPiece];
+    bool came = false;  // the run that is being added up
+    for (int64_t i0 = first; i0 < end; i0 += kPiece) {
+        const int count = static_cast<int>(end - i0 < kPiece ? end - i0 : kPiece);
+        // lane j: the key before the j-th token of these, so that lane count has the
+        // last one's and lane count + 1 the one behind; and the j-th token's place
+        const int64_t at = i0 - 1 + lane;
+        const uint32_t keys = at >= 0 && at < a.tokens && lane < count + 2 ? s.keys[at] : none + 1;
+        const uint32_t order = lane < count ? s.order[i0 + lane] : 0;
+        if (p.n <= 0) return;
+        uint32_t key = lane_value(keys, 1);
+        if (key == none) return;
+        if (i0 == first) came = lane_value(keys, 0) == key;
+        Raw8<DB> r[kPiece];
+        Raw8<TB == 0 ? 2 : TB> old[TB == 0 ? 1 : kPiece];
 #pragma unroll
-    for (int j = 0; j < kPiece; ++j) {
-        const uint32_t own = lane_value(keys, j + 1);
-        if (j >= count || own == none) continue;
-        r[j] = load8<DB>(a.dy, static_cast<int64_t>(lane_value(order, j)) * a.ld_dy + p.c, p.n);
-        if constexpr (TB != 0)
-            if (lane_value(keys, j + 2) != own) old[j] = old_row<TB>(a, own, p.c, p.n);
-    }
-#pragma unroll
-    for (int j = 0; j < kPiece; ++j) {
-        if (j >= count || key == none) continue;
-        float f[8];
-        widen8<DB>(r[j], a.dy_dtype == ZERO_BF16, f);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) sum[k] += f[k];
-        const uint32_t next = lane_value(keys, j + 2);
-        if (next == key && j + 1 < count) continue;
-        if (came || next == key) {
-            store8(s.parts, (2 * p.piece + (came ? 0 : 1)) * a.cols + p.c, p.n, ZERO_F32, sum);
-            if (!came && p.c == 0)
-                s.list[atomicAdd(s.crossing, 1u)] = static_cast<uint32_t>(p.piece);
-        } else {
-            put_row<TB>(a, key, p.c, p.n, old[TB == 0 ? 0 : j], sum);
+        for (int j = 0; j < kPiece; ++j) {
+            const uint32_t own = lane_value(keys, j + 1);
+            if (j >= count || own == none) continue;
+            r[j] = load8<DB>(a.dy, static_cast<int64_t>(lane_value(order, j)) * a.ld_dy + p.c, p.n);
+            if constexpr (TB != 0)
+                if (lane_value(keys, j + 2) != own) old[j] = old_row<TB>(a, own, p.c, p.n);
         }
 #pragma unroll
-        for (int k = 0; k < 8; ++k) sum[k] = 0.0f;
-        came = false;
-        key = next;
+        for (int j = 0; j < kPiece; ++j) {
+            if (j >= count || key == none) continue;
+            float f[8];
+            widen8<DB>(r[j], a.dy_dtype == ZERO_BF16, f);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) sum[k] += f[k];
+            const uint32_t next = lane_value(keys, j + 2);
+            if (next == key && i0 + j + 1 < end) continue;
+            if (came || next == key) {
+                store8(s.parts, (2 * p.piece + (came ? 0 : 1)) * a.cols + p.c, p.n, ZERO_F32, sum);
+                if (!came && p.c == 0)
+                    s.list[atomicAdd(s.crossing, 1u)] = static_cast<uint32_t>(p.piece);
+            } else {
+                put_row<TB>(a, key, p.c, p.n, old[TB == 0 ? 0 : j], sum);
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) sum[k] = 0.0f;
+            came = false;
+            key = next;
+        }
+        if constexpr (!LONG) return;
     }
 }
 
@@ -484,7 +493,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void embed_join_kernel(const Embed
     for (uint64_t job = blockIdx.x; job < jobs; job += gridDim.x) {
         const uint32_t run = static_cast<uint32_t>(job / slices);
         const int64_t piece = s.list[run];
-        const uint32_t key = s.keys[(piece + 1) * kPiece];
+        const uint32_t key = s.keys[(piece + 1) * s.length];
         const int64_t c = (static_cast<int64_t>(job - static_cast<uint64_t>(run) * slices) * 64 +
                            lane) * 8;
         const int64_t left = a.cols - c;
@@ -497,7 +506,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void embed_join_kernel(const Embed
         }
         for (int64_t first = piece + 1;; first += 64) {
             // how many of the next 64 pieces the run came into
-            const int64_t i = (first + lane) * kPiece;
+            const int64_t i = (first + lane) * s.length;
             const uint64_t in = __ballot(i < a.tokens && s.keys[i < a.tokens ? i : 0] == key);
             const int count = ~in ? __ffsll(static_cast<long long>(~in)) - 1 : 64;
             Raw8<4> r[64 / kJoinWaves];
@@ -531,7 +540,16 @@ __global__ __launch_bounds__(64 * kJoinWaves) void embed_join_kernel(const Embed
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-int64_t pieces(int64_t tokens) { return ceil_div(tokens, kPiece); }
+// Tokens in a piece: more than 16 where there are waves enough, 32 for each CU, since
+// a long run leaves a partial row in each piece (65536 tokens of 32000 x 4096: 63 us to
+// join them in pieces of 16, 23 in pieces of 64).
+int64_t piece_length(int64_t tokens, int64_t cols) {
+    int64_t length = kPiece;
+    while (length < 16 * kPiece && ceil_div(tokens, 2 * length) * ceil_div(cols, 512) >= 8192)
+        length *= 2;
+    return length;
+}
+int64_t pieces(int64_t tokens, int64_t cols) { return ceil_div(tokens, piece_length(tokens, cols)); }
 int64_t up16(int64_t n) { return (n + 15) & ~int64_t{15}; }
 int piece_shift(int64_t cols) { return cols <= 512 ? 6 : cols <= 1024 ? 7 : 8; }
 int64_t piece_slices(int64_t cols) { return ceil_div(cols, int64_t{8} << piece_shift(cols)); }
@@ -579,9 +597,9 @@ EmbedWorkspace embed_workspace(int64_t tokens, int64_t cols) {
     w.counts = at;
     at = up16(at + 4 * kBins * ceil_div(tokens, kSortItems));
     w.list = at;
-    at = up16(at + 4 * (1 + pieces(tokens)));
+    at = up16(at + 4 * (1 + pieces(tokens, cols)));
     w.parts = at;
-    w.bytes = at + 4 * 2 * pieces(tokens) * cols;
+    w.bytes = at + 4 * 2 * pieces(tokens, cols) * cols;
     return w;
 }
 
@@ -603,7 +621,7 @@ int64_t fill_tiles(int64_t vocab, int64_t cols, int64_t ld) {
 }  // namespace
 
 int64_t embed_backward_blocks(int64_t tokens, int64_t vocab, int64_t cols, int64_t ld_dt) {
-    const int64_t sum = ceil_div(pieces(tokens), kLanes >> piece_shift(cols)) * piece_slices(cols);
+    const int64_t sum = ceil_div(pieces(tokens, cols), kLanes >> piece_shift(cols)) * piece_slices(cols);
     const int64_t fill = 1 + fill_tiles(vocab, cols, ld_dt);
     return sum > fill ? sum : fill;
 }
@@ -633,16 +651,19 @@ hipError_t sum_and_join(const EmbedBackwardArgs& a, const Sorted& s, hipStream_t
     const int shift = piece_shift(a.cols);
     const int64_t slices = piece_slices(a.cols), wide = join_slices(a.cols);
     const hipError_t e = in_launches(
-        ceil_div(pieces(a.tokens), kLanes >> shift) * slices, kLanes,
+        ceil_div(pieces(a.tokens, a.cols), kLanes >> shift) * slices, kLanes,
         [&](int64_t first, uint32_t grid) {
             const Lanes l = {first, static_cast<uint32_t>(slices), shift};
+            auto run = [&](auto kernel) { kernel<<<grid, kLanes, 0, stream>>>(a, s, l); };
+            const bool is_long = s.length > kPiece;
             if (a.dy_dtype == ZERO_F32)
-                embed_sum_kernel<4, TB><<<grid, kLanes, 0, stream>>>(a, s, l);
-            else embed_sum_kernel<2, TB><<<grid, kLanes, 0, stream>>>(a, s, l);
+                is_long ? run(embed_sum_kernel<4, TB, true>) : run(embed_sum_kernel<4, TB, false>);
+            else
+                is_long ? run(embed_sum_kernel<2, TB, true>) : run(embed_sum_kernel<2, TB, false>);
             return hipGetLastError();
         });
-    if (e != hipSuccess || a.tokens <= kPiece) return e;
-    const int64_t jobs = (pieces(a.tokens) - 1) * wide;
+    if (e != hipSuccess || a.tokens <= s.length) return e;
+    const int64_t jobs = (pieces(a.tokens, a.cols) - 1) * wide;
     embed_join_kernel<TB><<<static_cast<uint32_t>(jobs < kJoinBlocks ? jobs : kJoinBlocks),
                             64 * kJoinWaves, 0, stream>>>(a, s, static_cast<uint32_t>(wide));
     return hipGetLastError();
@@ -667,6 +688,7 @@ hipError_t launch_embed_backward(const EmbedBackwardArgs& a, hipStream_t stream)
         p.crossing = reinterpret_cast<uint32_t*>(a.workspace + w.list);
         s.crossing = p.crossing;
         s.list = p.crossing + 1;
+        s.length = piece_length(a.tokens, a.cols);
         p.tokens = a.tokens; p.vocab = a.vocab; p.id_bytes = a.id_bytes;
         s.parts = reinterpret_cast<float*>(a.workspace + w.parts);
         if (a.tokens <= kSmall) {
