@@ -1,6 +1,7 @@
 """Build of libzerostep.so (the gfx950 kernels and the C-ABI host layer), of
-libzerotwin.so (the benchmark's measurement aids, zero_twin.h) and of
-workloads/libzerogen.so (the device side of the seeded input generators).
+libzerotwin.so (the benchmark's measurement aids, zero_twin.h), of
+workloads/libzerogen.so (the device side of the seeded input generators) and of
+_marshal.so (what the binding reads off tensors, host code).
 
 hipcc cross-compiles for gfx950 on any host, so this runs without a GPU.
 """
@@ -31,6 +32,9 @@ TWIN_SOURCES = [os.path.join(CSRC, "zero_twin.hip")]
 GEN_DIR = os.path.join(ROOT, "workloads", "csrc")
 GEN_LIB = os.path.join(ROOT, "workloads", "libzerogen.so")
 GEN_SOURCES = [os.path.join(GEN_DIR, "zero_gen.hip")]
+# host code against torch's and Python's headers, by g++
+MARSHAL_LIB = os.path.join(HERE, "_marshal.so")
+MARSHAL_SOURCE = os.path.join(CSRC, "marshal.cpp")
 ARCH = "gfx950"
 
 FLAGS = [
@@ -53,6 +57,22 @@ def hipcc() -> str:
         if cand and os.path.exists(cand):
             return cand
     raise RuntimeError("hipcc not found (set HIPCC or install ROCm)")
+
+
+def marshal_command(out: str) -> list:
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    gxx = shutil.which("g++")
+    if gxx is None:
+        raise RuntimeError("g++ not found")
+    return [gxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            "-isystem", os.path.join(root, "include"),
+            "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+            "-isystem", sysconfig.get_paths()["include"], "-I", INCLUDE, MARSHAL_SOURCE, "-o", out,
+            "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10"]
 
 
 def code_text(src: str) -> str:
@@ -121,15 +141,22 @@ def _run_all(commands, verbose: bool) -> None:
 
 
 def build(verbose: bool = False) -> str:
-    """Compile the three libraries for gfx950: each source to an object (hipcc
-    processes side by side), then each library from its objects, written
-    atomically."""
+    """Compile the three libraries for gfx950, each source to an object (hipcc
+    processes side by side), then each library from its objects, and the
+    binding's host library; each written atomically."""
     libs = ((LIB, SOURCES), (TWIN_LIB, TWIN_SOURCES), (GEN_LIB, GEN_SOURCES))
     compile_flags = [f for f in FLAGS if f != "-shared"]
     link_flags = [f"--offload-arch={ARCH}", "-fPIC", "-shared"]
     temps = []
     with tempfile.TemporaryDirectory(prefix="zerostep_build_") as objdir:
         try:
+            def temp(lib: str) -> str:
+                fd, tmp = tempfile.mkstemp(prefix=f".{os.path.basename(lib)}.", suffix=".tmp",
+                                           dir=os.path.dirname(lib))
+                os.close(fd)
+                temps.append(tmp)
+                return tmp
+
             compiles, links = [], []
             for lib, sources in libs:
                 objects = []
@@ -138,15 +165,12 @@ def build(verbose: bool = False) -> str:
                     objects.append(obj)
                     compiles.append([hipcc(), *compile_flags, "-I", INCLUDE, "-I", CSRC, "-I",
                                      GEN_DIR, "-o", obj, "-c", src])
-                name = os.path.basename(lib)
-                fd, tmp = tempfile.mkstemp(prefix=f".{name}.", suffix=".tmp",
-                                           dir=os.path.dirname(lib))
-                os.close(fd)
-                temps.append(tmp)
+                tmp = temp(lib)
                 links.append((lib, tmp, [hipcc(), *link_flags, *objects, "-o", tmp]))
-            _run_all(compiles, verbose)
+            marshal = temp(MARSHAL_LIB)
+            _run_all([*compiles, marshal_command(marshal)], verbose)
             _run_all([cmd for _, _, cmd in links], verbose)
-            for lib, tmp, _ in links:
+            for lib, tmp in (*((lib, tmp) for lib, tmp, _ in links), (MARSHAL_LIB, marshal)):
                 os.replace(tmp, lib)
         finally:
             for tmp in temps:
@@ -157,6 +181,6 @@ def build(verbose: bool = False) -> str:
 
 def ensure_built() -> str:
     """Build only if a library is missing."""
-    if not all(os.path.exists(p) for p in (LIB, TWIN_LIB, GEN_LIB)):
+    if not all(os.path.exists(p) for p in (LIB, TWIN_LIB, GEN_LIB, MARSHAL_LIB)):
         build()
     return LIB

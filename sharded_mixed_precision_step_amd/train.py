@@ -16,7 +16,7 @@ from typing import Optional, Tuple
 
 import torch
 
-from . import StepControl, ZeroStepError, _check, _ctl, lib
+from . import StepControl, ZeroStepError, _check, _ctl, _marshal, lib
 
 ZERO_F32, ZERO_F16, ZERO_BF16 = 0, 1, 2
 ZERO_E4M3, ZERO_E5M2 = 0, 1
@@ -74,9 +74,11 @@ _declare()
 
 
 # What a call looks at is written out below rather than wrapped in objects: a
-# short call's time is the host's.
+# short call's time is the host's.  The functions that read tensors are _marshal's
+# (csrc/marshal.cpp); these say what they do, and raise what there is to raise.
 
-def _mat(t: torch.Tensor, kinds: dict, dev: torch.device, name: str) -> Tuple[int, int, int]:
+def _mat_checked(t: torch.Tensor, kinds: dict, dev: torch.device,
+                 name: str) -> Tuple[int, int, int]:
     """(pointer, type code, row stride) of a matrix on dev.  A single row's
     stride says nothing: it counts as the row's length, rounded up to what the
     q8 layout asks of strides."""
@@ -97,14 +99,15 @@ def _mat(t: torch.Tensor, kinds: dict, dev: torch.device, name: str) -> Tuple[in
     return t.data_ptr(), code, ld
 
 
-def _like(t: torch.Tensor, shape, kinds: dict, dev: torch.device, name: str):
+def _like_checked(t: torch.Tensor, shape, kinds: dict, dev: torch.device, name: str):
     """_mat of a matrix of this shape."""
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    return _mat(t, kinds, dev, name)
+    return _mat_checked(t, kinds, dev, name)
 
 
-def _vec(t: torch.Tensor, n: int, kinds: dict, dev: torch.device, name: str) -> Tuple[int, int]:
+def _vec_checked(t: torch.Tensor, n: int, kinds: dict, dev: torch.device,
+                 name: str) -> Tuple[int, int]:
     """(pointer, type code) of a contiguous vector of n elements on dev."""
     code = kinds.get(t.dtype)
     if code is None:
@@ -118,17 +121,17 @@ def _vec(t: torch.Tensor, n: int, kinds: dict, dev: torch.device, name: str) -> 
     return t.data_ptr(), code
 
 
-def _q8(data: Optional[torch.Tensor], scales: Optional[torch.Tensor], rows: int, cols: int,
-        dev: torch.device, name: str, fmt: Optional[int] = None):
+def _q8_checked(data: Optional[torch.Tensor], scales: Optional[torch.Tensor], rows: int,
+                cols: int, dev: torch.device, name: str, fmt: Optional[int] = None):
     """(data pointer, ld, scale pointer, ld, format) of a q8 matrix."""
     if data is None or scales is None:
         if data is not None or scales is not None:
             raise ValueError(f"{name}: data and scales go together")
         return None, 0, None, 0, fmt
-    p, code, ld = _mat(data, _FP8, dev, name)
+    p, code, ld = _mat_checked(data, _FP8, dev, name)
     if fmt is not None and code != fmt:
         raise TypeError(f"{name} has dtype {data.dtype}, unlike the other output")
-    ps, _, lds = _mat(scales, _SCALE, dev, name)
+    ps, _, lds = _mat_checked(scales, _SCALE, dev, name)
     blocks = -(-cols // ZERO_Q8_BLOCK)
     have, wide = data.shape
     if have != rows or wide < blocks * ZERO_Q8_BLOCK:
@@ -139,6 +142,10 @@ def _q8(data: Optional[torch.Tensor], scales: Optional[torch.Tensor], rows: int,
         raise ValueError(f"scales of {name} have shape {tuple(scales.shape)}, expected "
                          f"{rows} rows of {-(-blocks // 4) * 4}")
     return p, ld, ps, lds, code
+
+
+_marshal.init(_mat_checked, _like_checked, _vec_checked, _q8_checked, _FP8, _SCALE)
+_mat, _like, _vec, _q8 = _marshal.mat, _marshal.like, _marshal.vec, _marshal.q8
 
 
 def _device(t: torch.Tensor) -> torch.device:
@@ -156,7 +163,7 @@ def _raw_stream(stream, dev: torch.device) -> int:
 
 def _run(fn, dev: torch.device, *args) -> None:
     """Make the call with dev current, as the library launches there."""
-    if dev.index == torch.cuda.current_device():
+    if dev.index == torch._C._cuda_getDevice():
         rc = fn(*args)
     else:
         with torch.cuda.device(dev):
