@@ -3,14 +3,13 @@
 // Forward: a gather, bound by the latency of id -> row -> store for few tokens
 // and by HBM for many.
 //
-// Backward: the tokens are sorted by their row of the table (a stable radix sort
-// of 9 bits a pass, so that equal ids keep the tokens' order), and the sorted
-// list is cut into pieces of 16 tokens, or more where there are very many.  A
-// workgroup adds up a piece's rows in
-// registers, run by run; a run that lies in one piece goes straight to its row
-// of the table, one that crosses into others leaves a partial row for each, which
-// a second kernel adds up in order.  So one frequent token is the work of many
-// workgroups, and the sums' order depends on the ids alone.
+// Backward of more than 512 tokens: they are sorted by their row of the table (a
+// stable radix sort of 9 bits a pass, so that equal ids keep the tokens' order), and
+// the sorted list is cut into pieces of 16 tokens, or more where there are very many.  A
+// workgroup adds up a piece's rows in registers, run by run; a run that lies in one
+// piece goes straight to its row of the table, one that crosses into others leaves a
+// partial row for each, which a second kernel adds up in order.  So one frequent token
+// is the work of many workgroups, and the sums' order depends on the ids alone.
 #include "zero_device.h"
 #include "zero_model_internal.h"
 
@@ -539,6 +538,112 @@ __global__ __launch_bounds__(64 * kJoinWaves) void embed_join_kernel(const Embed
     }
 }
 
+// ---- few tokens ------------------------------------------------------------
+// Up to kFew tokens need no sort and one launch.  A wave takes a token and 512
+// columns; the lanes compare all ids with its own, which says whether it is the first
+// with that id and, if so, which others it adds up, in order.  Other workgroups write
+// the zeros, of the rows that no id names.
+
+constexpr int kFew = 512, kFewKeys = kFew / 64;
+constexpr int kFewAtOnce = 8;
+
+struct Few {
+    uint32_t sum_blocks, token_slices;  // workgroups that add up; waves to a token
+    uint32_t rows, fill_slices;         // of the table; workgroups to a row or rows
+    int32_t shift;                      // 2^shift lanes to a row of zeros
+};
+
+template <int DB, int TB>
+__device__ __forceinline__ void few_sum(const EmbedBackwardArgs& a, const Few& f, int64_t job) {
+    __shared__ uint16_t lists[kLanes / 64][kFew];  // a wave's tokens with its id
+    const int lane = threadIdx.x & 63, n_ids = static_cast<int>(a.tokens);
+    const int token = static_cast<int>(static_cast<uint32_t>(job) / f.token_slices);
+    if (token >= n_ids) return;
+    const int64_t slice = static_cast<uint32_t>(job) - static_cast<uint32_t>(token) * f.token_slices;
+    const int64_t c = (slice * 64 + lane) * 8, left = a.cols - c;
+    const int n = static_cast<int>(left < 8 ? left : 8);
+    SortPass p = {};
+    p.ids = a.ids;
+    p.tokens = a.tokens; p.vocab = a.vocab; p.id_bytes = a.id_bytes;
+    uint32_t key[kFewKeys];
+    load_keys<kFewKeys, 64>(p, lane, key);
+    // the token's own key, then which others share it
+    uint32_t own = 0;
+#pragma unroll
+    for (int k = 0; k < kFewKeys; ++k)
+        if (k == token / 64) own = lane_value(key[k], token % 64);
+    if (own == static_cast<uint32_t>(a.vocab)) return;
+    uint16_t* list = lists[threadIdx.x / 64];
+    int count = 0;
+    bool first = true;
+#pragma unroll
+    for (int k = 0; k < kFewKeys; ++k) {
+        const uint64_t same = __ballot(key[k] == own && k * 64 + lane < n_ids);
+        const uint64_t earlier = k * 64 + 64 <= token ? ~uint64_t{0}
+                                 : k * 64 >= token ? 0 : (uint64_t{1} << (token - k * 64)) - 1;
+        if (same & earlier) first = false;
+        if (same >> lane & 1)
+            list[count + __popcll(same & ((uint64_t{1} << lane) - 1))] =
+                static_cast<uint16_t>(k * 64 + lane);
+        count += __popcll(same);
+    }
+    if (!first) return;
+    wave_fence();
+    Raw8<TB == 0 ? 2 : TB> old;
+    if constexpr (TB != 0) old = old_row<TB>(a, own, c, n);
+    float sum[8] = {};
+    for (int i0 = 0; i0 < count; i0 += kFewAtOnce) {
+        const uint32_t mine = list[i0 + lane < count ? i0 + lane : i0];
+        Raw8<DB> r[kFewAtOnce];
+#pragma unroll
+        for (int u = 0; u < kFewAtOnce; ++u)
+            if (i0 + u < count) r[u] = load8<DB>(a.dy, lane_value(mine, u) * a.ld_dy + c, n);
+#pragma unroll
+        for (int u = 0; u < kFewAtOnce; ++u) {
+            if (i0 + u >= count) continue;
+            float x[8];
+            widen8<DB>(r[u], a.dy_dtype == ZERO_BF16, x);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum[i] += x[i];
+        }
+    }
+    put_row<TB>(a, own, c, n, old, sum);
+}
+
+__device__ __forceinline__ void few_zeros(const EmbedBackwardArgs& a, const Few& f,
+                                          uint32_t block) {
+    __shared__ uint32_t named[kLanes];
+    const uint32_t group = block / f.fill_slices, per = kLanes >> f.shift;
+    const int64_t r0 = static_cast<int64_t>(group) * per;
+    named[threadIdx.x] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.tokens; i += kLanes) {
+        const int64_t id = load_id(a.ids, i, a.id_bytes);
+        if (id >= r0 && id < r0 + per) named[id - r0] = 1;
+    }
+    __syncthreads();
+    const uint32_t r = threadIdx.x >> f.shift;
+    const int64_t c = (static_cast<int64_t>(block - group * f.fill_slices) << f.shift |
+                       (threadIdx.x & ((1 << f.shift) - 1))) * 8;
+    const int64_t left = a.cols - c;
+    const float zero[8] = {};
+    if (r0 + r < f.rows && !named[r])
+        store8(a.dtable, (r0 + r) * a.ld_dt + c, static_cast<int>(left < 8 ? left : 8), a.dt_dtype,
+               zero);
+}
+
+template <int DB, int TB>
+__global__ __launch_bounds__(kLanes) void embed_few_kernel(const EmbedBackwardArgs a, const Few f,
+                                                           int64_t first) {
+    const int64_t block = first + blockIdx.x;
+    if (block < f.sum_blocks) {
+        few_sum<DB, TB>(a, f, block * (kLanes / 64) +
+                                  __builtin_amdgcn_readfirstlane(threadIdx.x / 64));
+    } else if constexpr (TB == 0) {
+        few_zeros(a, f, static_cast<uint32_t>(block - f.sum_blocks));
+    }
+}
+
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // Tokens in a piece: more than 16 where there are waves enough, 32 for each CU, since
 // a long run leaves a partial row in each piece (65536 tokens of 32000 x 4096: 63 us to
@@ -620,6 +725,26 @@ int64_t fill_tiles(int64_t vocab, int64_t cols, int64_t ld) {
 
 }  // namespace
 
+namespace {
+
+int few_shift(int64_t cols) {
+    int shift = 0;
+    while (shift < 8 && (int64_t{8} << shift) < cols) ++shift;
+    return shift;
+}
+int64_t few_sum_blocks(int64_t tokens, int64_t cols) {
+    return ceil_div(tokens * ceil_div(cols, 512), kLanes / 64);
+}
+int64_t few_fill_blocks(int64_t vocab, int64_t cols) {
+    return ceil_div(vocab, kLanes >> few_shift(cols)) * ceil_div(cols, int64_t{8} << few_shift(cols));
+}
+bool is_few(int64_t tokens, int64_t vocab, int64_t cols) {
+    return tokens > 0 && tokens <= kFew &&
+           few_sum_blocks(tokens, cols) + few_fill_blocks(vocab, cols) <= 0x7fffffff;
+}
+
+}  // namespace
+
 int64_t embed_backward_blocks(int64_t tokens, int64_t vocab, int64_t cols, int64_t ld_dt) {
     const int64_t sum = ceil_div(pieces(tokens, cols), kLanes >> piece_shift(cols)) * piece_slices(cols);
     const int64_t fill = 1 + fill_tiles(vocab, cols, ld_dt);
@@ -669,9 +794,30 @@ hipError_t sum_and_join(const EmbedBackwardArgs& a, const Sorted& s, hipStream_t
     return hipGetLastError();
 }
 
+template <int TB>
+hipError_t launch_few(const EmbedBackwardArgs& a, hipStream_t stream) {
+    Few f = {};
+    f.sum_blocks = static_cast<uint32_t>(few_sum_blocks(a.tokens, a.cols));
+    f.token_slices = static_cast<uint32_t>(ceil_div(a.cols, 512));
+    f.rows = static_cast<uint32_t>(a.vocab);
+    f.shift = few_shift(a.cols);
+    f.fill_slices = static_cast<uint32_t>(ceil_div(a.cols, int64_t{8} << f.shift));
+    return in_launches(f.sum_blocks + (TB == 0 ? few_fill_blocks(a.vocab, a.cols) : 0), kLanes,
+                       [&](int64_t first, uint32_t grid) {
+                           if (a.dy_dtype == ZERO_F32)
+                               embed_few_kernel<4, TB><<<grid, kLanes, 0, stream>>>(a, f, first);
+                           else embed_few_kernel<2, TB><<<grid, kLanes, 0, stream>>>(a, f, first);
+                           return hipGetLastError();
+                       });
+}
+
 }  // namespace
 
 hipError_t launch_embed_backward(const EmbedBackwardArgs& a, hipStream_t stream) {
+    if (is_few(a.tokens, a.vocab, a.cols)) {
+        if (!a.accumulate) return launch_few<0>(a, stream);
+        return a.dt_dtype == ZERO_F32 ? launch_few<4>(a, stream) : launch_few<2>(a, stream);
+    }
     Sorted s = {};
     SortPass p = {};
     int passes = 0;  // of the first launch's own sort
