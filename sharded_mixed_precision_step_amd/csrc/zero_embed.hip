@@ -425,7 +425,8 @@ __global__ __launch_bounds__(kLanes) void embed_sum_kernel(const EmbedBackwardAr
                                                            const Sorted s, const Lanes l) {
     const PieceAt p = piece_at(l, a.cols);
     const int64_t length = LONG ? s.length : kPiece, first = p.piece * length;
-    if (first >= a.tokens) return;
+    // a wave goes as a whole: lanes without columns hold keys that the others read
+    if (first >= a.tokens || __ballot(p.n > 0) == 0) return;
     const int64_t end = first + length < a.tokens ? first + length : a.tokens;
     const int lane = threadIdx.x % 64;
     const uint32_t none = static_cast<uint32_t>(a.vocab);
@@ -438,7 +439,6 @@ __global__ __launch_bounds__(kLanes) void embed_sum_kernel(const EmbedBackwardAr
         const int64_t at = i0 - 1 + lane;
         const uint32_t keys = at >= 0 && at < a.tokens && lane < count + 2 ? s.keys[at] : none + 1;
         const uint32_t order = lane < count ? s.order[i0 + lane] : 0;
-        if (p.n <= 0) return;
         uint32_t key = lane_value(keys, 1);
         if (key == none) return;
         if (i0 == first) came = lane_value(keys, 0) == key;
