@@ -124,6 +124,13 @@ __device__ __forceinline__ void settle8(Raw8<BYTES>& r, int c, int cols) {
     }
 }
 
+// Waits for a load: what stands behind it may be written where it read.
+template <int BYTES>
+__device__ __forceinline__ void arrived(const Raw8<BYTES>& r) {
+#pragma unroll
+    for (int k = 0; k < (BYTES == 4 ? 2 : 1); ++k) asm volatile("" ::"v"(r.v[k]) : "memory");
+}
+
 template <int BYTES>
 __device__ __forceinline__ void widen8(const Raw8<BYTES>& r, bool bf16, float (&f)[8]) {
     if constexpr (BYTES == 4) {

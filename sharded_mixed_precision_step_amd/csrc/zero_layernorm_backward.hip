@@ -29,7 +29,9 @@ struct Pack {
         h = load8<HB>(a.h, row * a.ld_h + c, 8);
         if constexpr (RB != 0) r = load8<RB>(a.dres, row * a.ld_dr + c, 8);
     }
-    // sums of g and g xhat, of the elements from `from` on
+    // Sums of g and g xhat, of the elements from `from` on.  Behind it all loads have
+    // arrived: dx may be any of the three, and its owner's pack may share elements with
+    // the row's last one.
     __device__ __forceinline__ void reduce(const LayerNormBackwardArgs& a, const float (&w)[8],
                                            int from, float mean, float rstd, float& sg,
                                            float& sgx) const {
@@ -42,6 +44,7 @@ struct Pack {
             sg += g;
             sgx = __builtin_fmaf(g, k >= from ? (x[k] - mean) * rstd : 0.0f, sgx);
         }
+        if constexpr (RB != 0) arrived(r);
     }
     __device__ __forceinline__ void finish(const LayerNormBackwardArgs& a, int64_t row, int c,
                                            const float (&w)[8], float mean, float rstd, float mg,
