@@ -82,6 +82,7 @@ struct SortPass {
     uint32_t* crossing;         // the list's length, cleared by the first launch
     int64_t tokens, vocab;
     int32_t id_bytes, shift;
+    bool scanned;               // the counts are sums already
 };
 
 // The keys of items i0 + r * STEP, all loads under way at once; past the end the
@@ -169,6 +170,35 @@ __global__ __launch_bounds__(kLanes) void sort_count_kernel(const SortPass a) {
         a.counts[static_cast<int64_t>(blockIdx.x) * kBins + d] = bins[d];
 }
 
+// Up to this many blocks, each adds up the others' counts by itself.
+constexpr uint32_t kUnscanned = 64;
+
+// counts[block][digit] becomes the earlier blocks' count of the digit; behind the last
+// block, all blocks' count.  64 digits a workgroup, a range of blocks each wave.
+constexpr int kScanWaves = 16;
+__global__ __launch_bounds__(64 * kScanWaves) void sort_scan_kernel(uint32_t* counts,
+                                                                    uint32_t blocks) {
+    __shared__ uint32_t sums[kScanWaves][64];
+    const uint32_t lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+    const uint32_t per = (blocks + kScanWaves - 1) / kScanWaves;
+    const uint32_t b0 = wave * per, b1 = b0 + per < blocks ? b0 + per : blocks;
+    uint32_t* own = counts + blockIdx.x * 64 + lane;
+    uint32_t sum = 0;
+#pragma unroll 16
+    for (uint32_t b = b0; b < b1; ++b) sum += own[static_cast<int64_t>(b) * kBins];
+    sums[wave][lane] = sum;
+    __syncthreads();
+    uint32_t at = 0;
+    for (uint32_t w = 0; w < wave; ++w) at += sums[w][lane];
+    if (wave == kScanWaves - 1) own[static_cast<int64_t>(blocks) * kBins] = at + sum;
+#pragma unroll 16
+    for (uint32_t b = b0; b < b1; ++b) {
+        const uint32_t n = own[static_cast<int64_t>(b) * kBins];
+        own[static_cast<int64_t>(b) * kBins] = at;
+        at += n;
+    }
+}
+
 // Places the items behind those of lower digits, of earlier blocks, waves and
 // rounds, and of lower lanes.
 __global__ __launch_bounds__(kLanes) void sort_scatter_kernel(const SortPass a) {
@@ -192,13 +222,21 @@ __global__ __launch_bounds__(kLanes) void sort_scatter_kernel(const SortPass a) 
     }
     // digits kPer * t ..: all blocks' items, and the earlier blocks'
     uint32_t all[kPer] = {}, before[kPer] = {};
-#pragma unroll 8
-    for (uint32_t b = 0; b < gridDim.x; ++b) {
+    if (a.scanned) {
 #pragma unroll
         for (int k = 0; k < kPer; ++k) {
-            const uint32_t n = a.counts[static_cast<int64_t>(b) * kBins + kPer * t + k];
-            all[k] += n;
-            before[k] += b < blockIdx.x ? n : 0;
+            before[k] = a.counts[static_cast<int64_t>(blockIdx.x) * kBins + kPer * t + k];
+            all[k] = a.counts[static_cast<int64_t>(gridDim.x) * kBins + kPer * t + k];
+        }
+    } else {
+#pragma unroll 8
+        for (uint32_t b = 0; b < gridDim.x; ++b) {
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) {
+                const uint32_t n = a.counts[static_cast<int64_t>(b) * kBins + kPer * t + k];
+                all[k] += n;
+                before[k] += b < blockIdx.x ? n : 0;
+            }
         }
     }
     __syncthreads();
@@ -700,7 +738,7 @@ EmbedWorkspace embed_workspace(int64_t tokens, int64_t cols) {
         at = up16(at + 4 * tokens);
     }
     w.counts = at;
-    at = up16(at + 4 * kBins * ceil_div(tokens, kSortItems));
+    at = up16(at + 4 * kBins * (1 + ceil_div(tokens, kSortItems)));
     w.list = at;
     at = up16(at + 4 * (1 + pieces(tokens, cols)));
     w.parts = at;
@@ -758,10 +796,13 @@ hipError_t sort_many(SortPass p, uint32_t* const (&keys)[2], uint32_t* const (&o
                      hipStream_t stream, Sorted* s) {
     const uint32_t grid = static_cast<uint32_t>(ceil_div(p.tokens, kSortItems));
     int to = 0;
+    p.scanned = grid > kUnscanned;
     for (p.shift = 0; p.vocab >> p.shift; p.shift += kDigit, to ^= 1) {
         p.keys_out = keys[to];
         p.order_out = order[to];
         sort_count_kernel<<<grid, kLanes, 0, stream>>>(p);
+        if (p.scanned)
+            sort_scan_kernel<<<kBins / 64, 64 * kScanWaves, 0, stream>>>(p.counts, grid);
         sort_scatter_kernel<<<grid, kLanes, 0, stream>>>(p);
         p.keys_in = keys[to];
         p.order_in = order[to];
