@@ -32,6 +32,8 @@ struct Pack {
             const float sum = __builtin_fmaf(dy[k] * w[k], x[k] * rstd, dot);
             dot = k >= from ? sum : dot;
         }
+        // dx may be dresidual, and a held row's last pack shares another lane's elements
+        if constexpr (RB != 0) arrived(r);
     }
     __device__ __forceinline__ void finish(const NormBackwardArgs& a, int64_t row, int c, int n,
                                            const float (&w)[8], float rstd, float mean,
