@@ -25,12 +25,6 @@ __device__ __forceinline__ int64_t load_id(const void* ids, int64_t i, int bytes
                       : static_cast<int64_t>(static_cast<const int32_t*>(ids)[i]);
 }
 
-__device__ __forceinline__ void load_row8(const void* p, int64_t i, int n, int dtype,
-                                          float (&f)[8]) {
-    if (dtype == ZERO_F32) widen8<4>(load8<4>(p, i, n), false, f);
-    else widen8<2>(load8<2>(p, i, n), dtype == ZERO_BF16, f);
-}
-
 // ---- forward ---------------------------------------------------------------
 
 // 2^shift lanes to a token, U packs of eight columns a lane.
@@ -79,7 +73,6 @@ struct SortPass {
     const void* ids;            // first pass: the keys come from here
     const uint32_t *keys_in, *order_in;
     uint32_t *keys_out, *order_out, *counts;
-    uint32_t* crossing;         // the list's length, cleared by the first launch
     int64_t tokens, vocab;
     int32_t id_bytes, shift;
     bool scanned;               // the counts are sums already
@@ -157,7 +150,6 @@ __device__ __forceinline__ void rank_items(const uint32_t (&key)[N], int shift, 
 __global__ __launch_bounds__(kLanes) void sort_count_kernel(const SortPass a) {
     __shared__ uint32_t bins[kBins];
     for (int d = threadIdx.x; d < kBins; d += kLanes) bins[d] = 0;
-    if (blockIdx.x == 0 && threadIdx.x == 0 && !a.keys_in) *a.crossing = 0;
     const int64_t i0 = static_cast<int64_t>(blockIdx.x) * kSortItems + threadIdx.x;
     uint32_t key[kSortRounds];
     load_keys<kSortRounds, kLanes>(a, i0, key);
@@ -325,7 +317,6 @@ __device__ void sort_small(const SortPass& a, int passes, uint32_t* lds) {
     const int i0 = wave * 64 * rounds + lane, left = n - wave * 64 * rounds;
     uint32_t key[kSmallRounds], at[kSmallRounds];
     uint16_t place[kSmallRounds];
-    if (t == 0) *a.crossing = 0;
     load_keys<kSmallRounds, 64>(a, i0, key);
 #pragma unroll
     for (int r = 0; r < kSmallRounds; ++r) place[r] = static_cast<uint16_t>(i0 + r * 64);
@@ -409,7 +400,6 @@ constexpr int kPiece = 16;                // sorted tokens whose rows are under 
 struct Sorted {
     const uint32_t *keys, *order;
     float* parts;                         // [2 * pieces][cols]
-    uint32_t *crossing, *list;            // pieces in which a run begins that goes on
     int64_t length;                       // tokens in a piece, a multiple of kPiece
 };
 
@@ -501,8 +491,6 @@ __global__ __launch_bounds__(kLanes) void embed_sum_kernel(const EmbedBackwardAr
             if (next == key && i0 + j + 1 < end) continue;
             if (came || next == key) {
                 store8(s.parts, (2 * p.piece + (came ? 0 : 1)) * a.cols + p.c, p.n, ZERO_F32, sum);
-                if (!came && p.c == 0)
-                    s.list[atomicAdd(s.crossing, 1u)] = static_cast<uint32_t>(p.piece);
             } else {
                 put_row<TB>(a, key, p.c, p.n, old[TB == 0 ? 0 : j], sum);
             }
@@ -515,65 +503,101 @@ __global__ __launch_bounds__(kLanes) void embed_sum_kernel(const EmbedBackwardAr
     }
 }
 
-// The runs that go on from a piece in which they began: 512 columns a workgroup,
-// whose waves take every kJoinWaves-th piece each, added up in the waves' order.  The
-// list's order is chance, each run's sum is not.
-constexpr int kJoinWaves = 8, kJoinBlocks = 512;
+// The runs that go on from the piece in which they began: a wave looks at 512 columns
+// of one piece, and adds up the partial rows of up to kShortRun more pieces by itself.
+// Of eight neighbouring pieces at most one begins a longer run: the workgroup's waves
+// take every kJoinWaves-th of its pieces each, added up in the waves' order.
+// (A list of such runs that the sums' kernel makes with an atomic counter costs 9 ns a
+// run: 200000 tokens of 50000 x 128 fp16 118 us for the
+// sums, 25 without.)
+constexpr int kJoinWaves = 8, kShortRun = 8;
 template <int TB>
 __global__ __launch_bounds__(64 * kJoinWaves) void embed_join_kernel(const EmbedBackwardArgs a,
-                                                                     const Sorted s,
+                                                                     const Sorted s, int64_t n_first,
                                                                      uint32_t slices) {
     __shared__ float sums[kJoinWaves][64][8];
-    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-    const uint32_t runs = *s.crossing;
-    const uint64_t jobs = static_cast<uint64_t>(runs) * slices;
-    for (uint64_t job = blockIdx.x; job < jobs; job += gridDim.x) {
-        const uint32_t run = static_cast<uint32_t>(job / slices);
-        const int64_t piece = s.list[run];
-        const uint32_t key = s.keys[(piece + 1) * s.length];
-        const int64_t c = (static_cast<int64_t>(job - static_cast<uint64_t>(run) * slices) * 64 +
-                           lane) * 8;
-        const int64_t left = a.cols - c;
-        const int n = static_cast<int>(left < 8 ? left : 8);
-        float sum[8] = {};
-        Raw8<TB == 0 ? 2 : TB> old;
-        if (wave == 0) {
+    __shared__ int64_t long_piece;
+    const int lane = threadIdx.x % 64;
+    const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x / 64));
+    const int64_t block = n_first + blockIdx.x, group = block / slices;
+    const int64_t piece = group * kJoinWaves + wave, end = (piece + 1) * s.length;
+    const int64_t c = ((block - group * slices) * 64 + lane) * 8, left = a.cols - c;
+    const int n = static_cast<int>(left < 8 ? left : 8);
+    const uint32_t none = static_cast<uint32_t>(a.vocab);
+    if (threadIdx.x == 0) long_piece = -1;
+    __syncthreads();
+    // lane 0: the key before the piece; lane 1: its last one; lane 2 + j: the first one
+    // of the j-th piece behind it
+    const int64_t at = lane == 0 ? end - s.length - 1 : lane == 1 ? end - 1
+                                                                  : end + (lane - 2) * s.length;
+    const uint32_t keys = at >= 0 && at < a.tokens ? s.keys[at] : none;
+    const uint32_t key = lane_value(keys, 1);
+    const uint64_t same = __ballot(keys == key) >> 2;
+    if (key != none && (piece == 0 || lane_value(keys, 0) != key) && (same & 1)) {
+        const int count = __ffsll(static_cast<long long>(~same)) - 1;
+        if (count > kShortRun) {
+            if (lane == 0) long_piece = piece;
+        } else {
+            Raw8<4> r[kShortRun + 1];
+            Raw8<TB == 0 ? 2 : TB> old;
+            r[0] = load8<4>(s.parts, (2 * piece + 1) * a.cols + c, n);
+#pragma unroll
+            for (int u = 1; u <= kShortRun; ++u)
+                if (u <= count) r[u] = load8<4>(s.parts, 2 * (piece + u) * a.cols + c, n);
             if constexpr (TB != 0) old = old_row<TB>(a, key, c, n);
-            load_row8(s.parts, (2 * piece + 1) * a.cols + c, n, ZERO_F32, sum);
-        }
-        for (int64_t first = piece + 1;; first += 64) {
-            // how many of the next 64 pieces the run came into
-            const int64_t i = (first + lane) * s.length;
-            const uint64_t in = __ballot(i < a.tokens && s.keys[i < a.tokens ? i : 0] == key);
-            const int count = ~in ? __ffsll(static_cast<long long>(~in)) - 1 : 64;
-            Raw8<4> r[64 / kJoinWaves];
+            float sum[8];
+            widen8<4>(r[0], false, sum);
 #pragma unroll
-            for (int u = 0; u < 64 / kJoinWaves; ++u) {
-                const int j = u * kJoinWaves + wave;
-                r[u] = load8<4>(s.parts, 2 * (first + j) * a.cols + c, j < count ? n : 0);
-            }
-#pragma unroll
-            for (int u = 0; u < 64 / kJoinWaves; ++u) {
+            for (int u = 1; u <= kShortRun; ++u) {
+                if (u > count) continue;
                 float f[8];
                 widen8<4>(r[u], false, f);
 #pragma unroll
                 for (int k = 0; k < 8; ++k) sum[k] += f[k];
             }
-            if (count < 64) break;
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) sums[wave][lane][k] = sum[k];
-        __syncthreads();
-        if (wave == 0) {
-#pragma unroll
-            for (int w = 1; w < kJoinWaves; ++w) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) sum[k] += sums[w][lane][k];
-            }
             put_row<TB>(a, key, c, n, old, sum);
         }
-        __syncthreads();  // before the next job's sums
     }
+    __syncthreads();
+    const int64_t from = long_piece;
+    if (from < 0) return;
+    const uint32_t run = s.keys[(from + 1) * s.length];
+    float sum[8] = {};
+    Raw8<TB == 0 ? 2 : TB> old;
+    if (wave == 0) {
+        if constexpr (TB != 0) old = old_row<TB>(a, run, c, n);
+        widen8<4>(load8<4>(s.parts, (2 * from + 1) * a.cols + c, n), false, sum);
+    }
+    for (int64_t first = from + 1;; first += 64) {
+        // how many of the next 64 pieces the run came into
+        const int64_t i = (first + lane) * s.length;
+        const uint64_t in = __ballot(i < a.tokens && s.keys[i < a.tokens ? i : 0] == run);
+        const int count = ~in ? __ffsll(static_cast<long long>(~in)) - 1 : 64;
+        Raw8<4> r[64 / kJoinWaves];
+#pragma unroll
+        for (int u = 0; u < 64 / kJoinWaves; ++u) {
+            const int j = u * kJoinWaves + wave;
+            r[u] = load8<4>(s.parts, 2 * (first + j) * a.cols + c, j < count ? n : 0);
+        }
+#pragma unroll
+        for (int u = 0; u < 64 / kJoinWaves; ++u) {
+            float f[8];
+            widen8<4>(r[u], false, f);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) sum[k] += f[k];
+        }
+        if (count < 64) break;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sums[wave][lane][k] = sum[k];
+    __syncthreads();
+    if (wave != 0) return;
+#pragma unroll
+    for (int w = 1; w < kJoinWaves; ++w) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) sum[k] += sums[w][lane][k];
+    }
+    put_row<TB>(a, run, c, n, old, sum);
 }
 
 // ---- few tokens ------------------------------------------------------------
@@ -684,8 +708,8 @@ __global__ __launch_bounds__(kLanes) void embed_few_kernel(const EmbedBackwardAr
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // Tokens in a piece: more than 16 where there are waves enough, 32 for each CU, since
-// a long run leaves a partial row in each piece (65536 tokens of 32000 x 4096: 63 us to
-// join them in pieces of 16, 23 in pieces of 64).
+// a long run leaves a partial row in each piece (65536 tokens of 32000 x 4096 fp16 26 us
+// to join them in pieces of 16, 9 in pieces of 64; 16777216 of 50000 x 8 610 and 40).
 int64_t piece_length(int64_t tokens, int64_t cols) {
     int64_t length = kPiece;
     while (length < 16 * kPiece && ceil_div(tokens, 2 * length) * ceil_div(cols, 512) >= 8192)
@@ -697,6 +721,9 @@ int64_t up16(int64_t n) { return (n + 15) & ~int64_t{15}; }
 int piece_shift(int64_t cols) { return cols <= 512 ? 6 : cols <= 1024 ? 7 : 8; }
 int64_t piece_slices(int64_t cols) { return ceil_div(cols, int64_t{8} << piece_shift(cols)); }
 int64_t join_slices(int64_t cols) { return ceil_div(cols, 512); }
+int64_t join_blocks(int64_t tokens, int64_t cols) {
+    return ceil_div(pieces(tokens, cols), kJoinWaves) * join_slices(cols);
+}
 
 }  // namespace
 
@@ -739,8 +766,6 @@ EmbedWorkspace embed_workspace(int64_t tokens, int64_t cols) {
     }
     w.counts = at;
     at = up16(at + 4 * kBins * (1 + ceil_div(tokens, kSortItems)));
-    w.list = at;
-    at = up16(at + 4 * (1 + pieces(tokens, cols)));
     w.parts = at;
     w.bytes = at + 4 * 2 * pieces(tokens, cols) * cols;
     return w;
@@ -785,8 +810,8 @@ bool is_few(int64_t tokens, int64_t vocab, int64_t cols) {
 
 int64_t embed_backward_blocks(int64_t tokens, int64_t vocab, int64_t cols, int64_t ld_dt) {
     const int64_t sum = ceil_div(pieces(tokens, cols), kLanes >> piece_shift(cols)) * piece_slices(cols);
-    const int64_t fill = 1 + fill_tiles(vocab, cols, ld_dt);
-    return sum > fill ? sum : fill;
+    const int64_t fill = 1 + fill_tiles(vocab, cols, ld_dt), join = join_blocks(tokens, cols);
+    return sum > fill ? (sum > join ? sum : join) : (fill > join ? fill : join);
 }
 
 namespace {
@@ -815,7 +840,7 @@ hipError_t sort_many(SortPass p, uint32_t* const (&keys)[2], uint32_t* const (&o
 template <int TB>
 hipError_t sum_and_join(const EmbedBackwardArgs& a, const Sorted& s, hipStream_t stream) {
     const int shift = piece_shift(a.cols);
-    const int64_t slices = piece_slices(a.cols), wide = join_slices(a.cols);
+    const int64_t slices = piece_slices(a.cols);
     const hipError_t e = in_launches(
         ceil_div(pieces(a.tokens, a.cols), kLanes >> shift) * slices, kLanes,
         [&](int64_t first, uint32_t grid) {
@@ -829,10 +854,12 @@ hipError_t sum_and_join(const EmbedBackwardArgs& a, const Sorted& s, hipStream_t
             return hipGetLastError();
         });
     if (e != hipSuccess || a.tokens <= s.length) return e;
-    const int64_t jobs = (pieces(a.tokens, a.cols) - 1) * wide;
-    embed_join_kernel<TB><<<static_cast<uint32_t>(jobs < kJoinBlocks ? jobs : kJoinBlocks),
-                            64 * kJoinWaves, 0, stream>>>(a, s, static_cast<uint32_t>(wide));
-    return hipGetLastError();
+    return in_launches(join_blocks(a.tokens, a.cols), 64 * kJoinWaves,
+                       [&](int64_t first, uint32_t grid) {
+                           embed_join_kernel<TB><<<grid, 64 * kJoinWaves, 0, stream>>>(
+                               a, s, first, static_cast<uint32_t>(join_slices(a.cols)));
+                           return hipGetLastError();
+                       });
 }
 
 template <int TB>
@@ -872,9 +899,6 @@ hipError_t launch_embed_backward(const EmbedBackwardArgs& a, hipStream_t stream)
         }
         p.ids = a.ids;
         p.counts = reinterpret_cast<uint32_t*>(a.workspace + w.counts);
-        p.crossing = reinterpret_cast<uint32_t*>(a.workspace + w.list);
-        s.crossing = p.crossing;
-        s.list = p.crossing + 1;
         s.length = piece_length(a.tokens, a.cols);
         p.tokens = a.tokens; p.vocab = a.vocab; p.id_bytes = a.id_bytes;
         s.parts = reinterpret_cast<float*>(a.workspace + w.parts);

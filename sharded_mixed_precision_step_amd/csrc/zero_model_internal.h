@@ -25,10 +25,9 @@ int64_t embed_blocks(int64_t tokens, int64_t cols);  // workgroups of one call
 hipError_t launch_embed(const EmbedArgs& a, hipStream_t stream);
 
 // The backward's workspace: sorted keys and places twice (the passes of the
-// sort go back and forth), digit counts of the sort's blocks, a list of runs and its
-// length, partial rows.
+// sort go back and forth), digit counts of the sort's blocks, partial rows.
 struct EmbedWorkspace {
-    int64_t keys[2], order[2], counts, list, parts, bytes;  // byte offsets; total
+    int64_t keys[2], order[2], counts, parts, bytes;  // byte offsets; total
 };
 EmbedWorkspace embed_workspace(int64_t tokens, int64_t cols);
 struct EmbedBackwardArgs {
