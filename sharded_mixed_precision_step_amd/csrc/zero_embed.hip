@@ -278,13 +278,14 @@ constexpr int64_t kSmall = kStartLanes * kSmallRounds;  // tokens that one workg
 
 struct Fill {
     void* p;
-    int64_t cols, ld;
+    int64_t cols, ld;          // in halves, an fp32 column two of them
     uint32_t rows, slices;     // workgroups to a row; to 2^(10 - shift) rows if 1
-    int32_t dtype, shift;      // 2^shift lanes to a row
+    int32_t shift;             // 2^shift lanes to a row
 };
 
-// One pack a lane and workgroups in order: HBM takes plain stores best one after
-// another (1 GiB 171 us; 178 to 198 with four packs a lane or workgroups that go on).
+// One pack of 16 bytes a lane and workgroups in order: HBM takes plain stores best one
+// after another (1 GiB 171 us; 178 to 198 with four packs a lane or workgroups that go
+// on; 128 MB of fp32 26 us with two packs a lane, 21 with one).
 __device__ __forceinline__ void fill_zeros(const Fill& f, int64_t tile) {
     const float zero[8] = {};
     int64_t row = 0, c = tile * (8 * kStartLanes) + threadIdx.x * 8;
@@ -296,7 +297,7 @@ __device__ __forceinline__ void fill_zeros(const Fill& f, int64_t tile) {
         if (row >= f.rows) return;
     }
     const int64_t left = f.cols - c;
-    store8(f.p, row * f.ld + c, static_cast<int>(left < 8 ? left : 8), f.dtype, zero);
+    store8(f.p, row * f.ld + c, static_cast<int>(left < 8 ? left : 8), ZERO_F16, zero);
 }
 
 // All passes over up to kSmall tokens by one workgroup, the items in registers
@@ -612,6 +613,7 @@ constexpr int kFewAtOnce = 8;
 struct Few {
     uint32_t sum_blocks, token_slices;  // workgroups that add up; waves to a token
     uint32_t rows, fill_slices;         // of the table; workgroups to a row or rows
+    int64_t halves;                     // in a row, an fp32 column two of them
     int32_t shift;                      // 2^shift lanes to a row of zeros
 };
 
@@ -687,11 +689,11 @@ __device__ __forceinline__ void few_zeros(const EmbedBackwardArgs& a, const Few&
     const uint32_t r = threadIdx.x >> f.shift;
     const int64_t c = (static_cast<int64_t>(block - group * f.fill_slices) << f.shift |
                        (threadIdx.x & ((1 << f.shift) - 1))) * 8;
-    const int64_t left = a.cols - c;
+    const int64_t left = f.halves - c;
+    const int64_t ld = a.dt_dtype == ZERO_F32 ? 2 * a.ld_dt : a.ld_dt;
     const float zero[8] = {};
     if (r0 + r < f.rows && !named[r])
-        store8(a.dtable, (r0 + r) * a.ld_dt + c, static_cast<int>(left < 8 ? left : 8), a.dt_dtype,
-               zero);
+        store8(a.dtable, (r0 + r) * ld + c, static_cast<int>(left < 8 ? left : 8), ZERO_F16, zero);
 }
 
 template <int DB, int TB>
@@ -773,7 +775,9 @@ EmbedWorkspace embed_workspace(int64_t tokens, int64_t cols) {
 
 namespace {
 
-// The zeros' workgroups: of a table whose rows leave no gap, of one with strided rows.
+// The zeros' workgroups, in halves of 16 bits: of a table whose rows leave no gap, of
+// one with strided rows.
+int64_t halves(int64_t cols, int32_t dtype) { return dtype == ZERO_F32 ? 2 * cols : cols; }
 bool gapless(int64_t vocab, int64_t cols, int64_t ld) { return ld == cols || vocab == 1; }
 int fill_shift(int64_t cols) {
     int shift = 0;
@@ -801,16 +805,18 @@ int64_t few_sum_blocks(int64_t tokens, int64_t cols) {
 int64_t few_fill_blocks(int64_t vocab, int64_t cols) {
     return ceil_div(vocab, kLanes >> few_shift(cols)) * ceil_div(cols, int64_t{8} << few_shift(cols));
 }
-bool is_few(int64_t tokens, int64_t vocab, int64_t cols) {
+bool is_few(int64_t tokens, int64_t vocab, int64_t cols, int32_t dt_dtype) {
     return tokens > 0 && tokens <= kFew &&
-           few_sum_blocks(tokens, cols) + few_fill_blocks(vocab, cols) <= 0x7fffffff;
+           few_sum_blocks(tokens, cols) + few_fill_blocks(vocab, halves(cols, dt_dtype)) <= 0x7fffffff;
 }
 
 }  // namespace
 
-int64_t embed_backward_blocks(int64_t tokens, int64_t vocab, int64_t cols, int64_t ld_dt) {
+int64_t embed_backward_blocks(int64_t tokens, int64_t vocab, int64_t cols, int64_t ld_dt,
+                              int32_t dt_dtype) {
     const int64_t sum = ceil_div(pieces(tokens, cols), kLanes >> piece_shift(cols)) * piece_slices(cols);
-    const int64_t fill = 1 + fill_tiles(vocab, cols, ld_dt), join = join_blocks(tokens, cols);
+    const int64_t fill = 1 + fill_tiles(vocab, halves(cols, dt_dtype), halves(ld_dt, dt_dtype));
+    const int64_t join = join_blocks(tokens, cols);
     return sum > fill ? (sum > join ? sum : join) : (fill > join ? fill : join);
 }
 
@@ -868,9 +874,10 @@ hipError_t launch_few(const EmbedBackwardArgs& a, hipStream_t stream) {
     f.sum_blocks = static_cast<uint32_t>(few_sum_blocks(a.tokens, a.cols));
     f.token_slices = static_cast<uint32_t>(ceil_div(a.cols, 512));
     f.rows = static_cast<uint32_t>(a.vocab);
-    f.shift = few_shift(a.cols);
-    f.fill_slices = static_cast<uint32_t>(ceil_div(a.cols, int64_t{8} << f.shift));
-    return in_launches(f.sum_blocks + (TB == 0 ? few_fill_blocks(a.vocab, a.cols) : 0), kLanes,
+    f.halves = halves(a.cols, a.dt_dtype);
+    f.shift = few_shift(f.halves);
+    f.fill_slices = static_cast<uint32_t>(ceil_div(f.halves, int64_t{8} << f.shift));
+    return in_launches(f.sum_blocks + (TB == 0 ? few_fill_blocks(a.vocab, f.halves) : 0), kLanes,
                        [&](int64_t first, uint32_t grid) {
                            if (a.dy_dtype == ZERO_F32)
                                embed_few_kernel<4, TB><<<grid, kLanes, 0, stream>>>(a, f, first);
@@ -882,7 +889,7 @@ hipError_t launch_few(const EmbedBackwardArgs& a, hipStream_t stream) {
 }  // namespace
 
 hipError_t launch_embed_backward(const EmbedBackwardArgs& a, hipStream_t stream) {
-    if (is_few(a.tokens, a.vocab, a.cols)) {
+    if (is_few(a.tokens, a.vocab, a.cols, a.dt_dtype)) {
         if (!a.accumulate) return launch_few<0>(a, stream);
         return a.dt_dtype == ZERO_F32 ? launch_few<4>(a, stream) : launch_few<2>(a, stream);
     }
@@ -920,14 +927,14 @@ hipError_t launch_embed_backward(const EmbedBackwardArgs& a, hipStream_t stream)
     if (!a.accumulate) {
         // rows without a gap between them are one long row
         const bool whole = gapless(a.vocab, a.cols, a.ld_dt);
+        const int64_t cols = halves(a.cols, a.dt_dtype);
         f.p = a.dtable;
-        f.dtype = a.dt_dtype;
-        f.ld = a.ld_dt;
+        f.ld = halves(a.ld_dt, a.dt_dtype);
         f.rows = whole ? 1 : static_cast<uint32_t>(a.vocab);
-        f.cols = whole ? a.vocab * a.cols : a.cols;
-        f.shift = fill_shift(a.cols);
-        f.slices = static_cast<uint32_t>(fill_slices(a.cols));
-        tiles = fill_tiles(a.vocab, a.cols, a.ld_dt);
+        f.cols = whole ? a.vocab * cols : cols;
+        f.shift = fill_shift(cols);
+        f.slices = static_cast<uint32_t>(fill_slices(cols));
+        tiles = fill_tiles(a.vocab, cols, f.ld);
     }
     const hipError_t e = in_launches(
         tiles + (passes > 0), kStartLanes, [&](int64_t first, uint32_t grid) {

@@ -215,7 +215,8 @@ int zero_embed_backward(const void* dy, int32_t dy_dtype, int64_t ld_dy, const v
     for (int o = 0; o < n_out; ++o)
         if ((rc = check_apart_but(outs[o], ins, n_in, 0u, who))) return rc;
     if ((rc = check_outputs(outs, n_out, who))) return rc;
-    if (zero::embed_backward_blocks(tokens, vocab, cols, ld_dt) > kMaxGrid) return too_many(who);
+    if (zero::embed_backward_blocks(tokens, vocab, cols, ld_dt, dt_dtype) > kMaxGrid)
+        return too_many(who);
     zero::EmbedBackwardArgs a = {};
     a.dy = dy; a.ids = ids;
     a.tokens = tokens; a.vocab = vocab; a.cols = cols; a.ld_dy = ld_dy; a.ld_dt = ld_dt;

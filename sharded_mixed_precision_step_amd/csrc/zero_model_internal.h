@@ -39,7 +39,8 @@ struct EmbedBackwardArgs {
     char* workspace;               // embed_workspace(tokens, cols).bytes
 };
 // Workgroups of the largest of a call's launches.
-int64_t embed_backward_blocks(int64_t tokens, int64_t vocab, int64_t cols, int64_t ld_dt);
+int64_t embed_backward_blocks(int64_t tokens, int64_t vocab, int64_t cols, int64_t ld_dt,
+                              int32_t dt_dtype);
 hipError_t launch_embed_backward(const EmbedBackwardArgs& a, hipStream_t stream);
 
 struct LayerNormArgs {

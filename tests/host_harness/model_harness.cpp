@@ -104,7 +104,7 @@ EmbedWorkspace embed_workspace(int64_t tokens, int64_t cols) {
     w.bytes = 20 * tokens + (tokens + 15) / 16 * 8 * cols;
     return w;
 }
-int64_t embed_backward_blocks(int64_t tokens, int64_t vocab, int64_t cols, int64_t) {
+int64_t embed_backward_blocks(int64_t tokens, int64_t vocab, int64_t cols, int64_t, int32_t) {
     return (tokens + 15) / 16 + (vocab + 7) / 8 * ((cols + 8191) / 8192);
 }
 int32_t layernorm_backward_parts(int64_t rows, int32_t) {
