@@ -70,13 +70,14 @@ struct Place {
     bool live;    // the row exists and the column is inside the padded row
     int n;        // elements of the pack, may be <= 0
 };
-__device__ __forceinline__ Place place(int64_t block, int shift, uint32_t slices, int64_t rows,
+__device__ __forceinline__ Place place(int64_t first, int shift, uint32_t slices, int64_t rows,
                                        int64_t cols) {
-    const int lanes = 1 << shift;
-    const int64_t group = block / slices;
+    const uint32_t block = static_cast<uint32_t>(first + blockIdx.x);  // all of them fit
+    const uint32_t group = block / slices;
     Place p;
-    p.row = group * (kLanes >> shift) + (threadIdx.x >> shift);
-    p.c = ((block - group * slices) * lanes + (threadIdx.x & (lanes - 1))) * 8;
+    p.row = static_cast<int64_t>(group) * (kLanes >> shift) + (threadIdx.x >> shift);
+    p.c = (static_cast<int64_t>(block - group * slices) << shift |
+           (threadIdx.x & ((1 << shift) - 1))) * 8;
     const int64_t padded = (cols + 127) & ~int64_t{127}, left = cols - p.c;
     p.live = p.row < rows && p.c < padded;
     p.n = p.live ? static_cast<int>(left < 8 ? left : 8) : 0;
@@ -101,7 +102,7 @@ __device__ __forceinline__ void put_q8(uint8_t* q, int64_t ld_q, uint8_t* s, int
 template <int KIND, int XB, bool UP>
 __global__ __launch_bounds__(kLanes) void act_kernel(const ActArgs a, int64_t first, int shift,
                                                      uint32_t slices) {
-    const Place p = place(first + blockIdx.x, shift, slices, a.rows, a.cols);
+    const Place p = place(first, shift, slices, a.rows, a.cols);
     const bool bf16 = a.x_dtype == ZERO_BF16;
     const Raw8<XB> rg = load8<XB>(a.gate, p.row * a.ld_g + p.c, p.n);
     Raw8<XB> ru;
@@ -149,7 +150,7 @@ template <int KIND, int FMT, int DB, bool UP>
 __global__ __launch_bounds__(kLanes) void act_backward_kernel(const ActBackwardArgs a,
                                                               int64_t first, int shift,
                                                               uint32_t slices) {
-    const Place p = place(first + blockIdx.x, shift, slices, a.rows, a.cols);
+    const Place p = place(first, shift, slices, a.rows, a.cols);
     if (p.n <= 0) return;
     const int64_t block = p.c / 128;
     const u32x2 qg = *reinterpret_cast<const u32x2*>(a.gate_q + p.row * a.ld_gq + p.c);

@@ -415,11 +415,13 @@ struct PieceAt {
     int n;
 };
 __device__ __forceinline__ PieceAt piece_at(const Lanes& l, int64_t cols) {
-    const int64_t block = l.first + blockIdx.x, group = block / l.slices;
+    const uint32_t block = static_cast<uint32_t>(l.first + blockIdx.x);  // all of them fit
+    const uint32_t group = block / l.slices;
     PieceAt p;
-    p.piece = group * (kLanes >> l.shift) +
+    p.piece = static_cast<int64_t>(group) * (kLanes >> l.shift) +
               __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> l.shift));
-    p.c = ((block - group * l.slices) << l.shift | (threadIdx.x & ((1 << l.shift) - 1))) * 8;
+    p.c = (static_cast<int64_t>(block - group * l.slices) << l.shift |
+           (threadIdx.x & ((1 << l.shift) - 1))) * 8;
     const int64_t left = cols - p.c;
     p.n = static_cast<int>(left < 8 ? left : 8);
     return p;
@@ -520,9 +522,12 @@ __global__ __launch_bounds__(64 * kJoinWaves) void embed_join_kernel(const Embed
     __shared__ int64_t long_piece;
     const int lane = threadIdx.x % 64;
     const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x / 64));
-    const int64_t block = n_first + blockIdx.x, group = block / slices;
-    const int64_t piece = group * kJoinWaves + wave, end = (piece + 1) * s.length;
-    const int64_t c = ((block - group * slices) * 64 + lane) * 8, left = a.cols - c;
+    const uint32_t block = static_cast<uint32_t>(n_first + blockIdx.x);  // all of them fit
+    const uint32_t group = block / slices;
+    const int64_t piece = static_cast<int64_t>(group) * kJoinWaves + wave;
+    const int64_t end = (piece + 1) * s.length;
+    const int64_t c = (static_cast<int64_t>(block - group * slices) * 64 + lane) * 8;
+    const int64_t left = a.cols - c;
     const int n = static_cast<int>(left < 8 ? left : 8);
     const uint32_t none = static_cast<uint32_t>(a.vocab);
     if (threadIdx.x == 0) long_piece = -1;
