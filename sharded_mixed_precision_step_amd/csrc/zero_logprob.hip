@@ -9,9 +9,9 @@
 // and by few others.  Packs of eight whose largest reaches it are noted in LDS as the
 // row goes by, so that it is read once; the top-th largest of many such maxima is a
 // closer border, and only the packs that reach that one are looked into.  Counting how
-// many come before each of their logits, by value and place, orders them.  A row with
-// too many on the border (long ties, or logits that rise along the row) is read again,
-// and its border found by bisection.
+// many come before each of their logits, by value and place, orders them.  Where too many
+// lie on the border, as in long ties, the row is read again for the exact value of the
+// top-th largest, and its ties are taken in the order of their places.
 #include "zero_device.h"
 #include "zero_model_internal.h"
 
@@ -101,16 +101,22 @@ __device__ __forceinline__ uint32_t order_key(float v) {
 __device__ __forceinline__ float key_value(uint32_t key) {
     return as_float(key ^ (key >> 31 ? 0x80000000u : 0xffffffffu));
 }
+// Low bits of a key that a border leaves out, for fewer steps (with those that fp16 has
+// 4096 x 131072 273 us to 260); and those that no value of the type has.
+constexpr int kCoarse = 16;
+template <int DT>
+constexpr int kExact = DT == ZERO_F32 ? 0 : DT == ZERO_F16 ? 13 : 16;
+
 constexpr int kGroups = 256;      // lane groups with a maximum each
 constexpr int kWide = 160;        // more packs or logits get a closer border first
 constexpr int kCollected = 8 * kWide + 16, kRanked = 256;
 
-// Of the numbers of 16 bits that a wave's lanes hold: the largest that at least `top`
+// Of the numbers of BITS bits that a wave's lanes hold: the largest that at least `top`
 // of them reach; 0 if none but 0 is.
-template <int N>
+template <int BITS, int N>
 __device__ __forceinline__ uint32_t nth_largest(const uint32_t (&v)[N], int top) {
     uint32_t key = 0;
-    for (int b = 15; b >= 0; --b) {
+    for (int b = BITS - 1; b >= 0; --b) {
         const uint32_t up = key | 1u << b;
         int count = 0;
 #pragma unroll
@@ -128,20 +134,8 @@ struct Row {
     float edge_x;
 };
 
-// Calls f(value, place) for each of the lane's logits, read again.
-template <int B, int T, class F>
-__device__ __forceinline__ void for_each(const Row& row, bool bf16, F f) {
-#pragma unroll 1
-    for (int p = threadIdx.x; p < row.packs; p += T) {
-        float v[8];
-        widen8<B>(load_aligned<B>(row.body + static_cast<int64_t>(p) * 8 * B), bf16, v);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) f(v[k], row.head + 8 * p + k);
-    }
-    if (row.edge >= 0) f(row.edge_x, row.edge);
-}
-
-// What the alternatives need in LDS.
+// What the alternatives need in LDS: 29 KB with 2,048 packs, so that five workgroups share
+// a CU.
 template <int PACKS>
 struct Tops {
     static constexpr int kPacks = PACKS;
@@ -151,7 +145,7 @@ struct Tops {
     float group_max[kGroups];
     float border;
     uint32_t n_packs, n, n_ranked;
-    uint32_t reach[2][16];
+    uint32_t reach[2][3][16];
 };
 
 // Larger entries come first: a value, then the places left over.
@@ -171,11 +165,18 @@ __device__ __forceinline__ void push(uint64_t* list, uint32_t& n, int room, uint
     if (at < static_cast<uint32_t>(room)) list[at] = e;
 }
 
-// The value that a key of 16 bits begins with; every finite value for 0, since -inf
-// is no alternative.
-__device__ __forceinline__ float border_value(uint32_t key16) {
-    const float v = key_value(key16 << 16);
-    return key16 <= 0x007fu ? kLowest : v;
+// The lowest value whose key without SHIFT bits is this; the lowest finite one for the
+// keys below, since -inf is no alternative.
+template <int SHIFT>
+__device__ __forceinline__ float border_value(uint32_t key) {
+    return key <= 0x007fffffu >> SHIFT ? kLowest : key_value(key << SHIFT);
+}
+
+// The value itself, where SHIFT bits are none that a value of the type has: a negative
+// one's key ends in ones.
+template <int SHIFT>
+__device__ __forceinline__ float exact_value(uint32_t key) {
+    return key_value(key << SHIFT | (key >> (31 - SHIFT) ? 0u : (1u << SHIFT) - 1));
 }
 
 // A border that the row's `top` largest reach, from the lanes' maxima.
@@ -190,9 +191,10 @@ __device__ __forceinline__ float first_border(Tops& s, float lane_max, int top) 
     if (t < 64) {
         uint32_t v[kGroups / 64];
 #pragma unroll
-        for (int i = 0; i < kGroups / 64; ++i) v[i] = order_key(s.group_max[i * 64 + t]) >> 16;
-        const uint32_t key = nth_largest(v, top);
-        if (t == 0) s.border = border_value(key);
+        for (int i = 0; i < kGroups / 64; ++i)
+            v[i] = order_key(s.group_max[i * 64 + t]) >> kCoarse;
+        const uint32_t key = nth_largest<32 - kCoarse>(v, top);
+        if (t == 0) s.border = border_value<kCoarse>(key);
     }
     __syncthreads();
     return s.border;
@@ -206,10 +208,10 @@ __device__ __forceinline__ float closer(const uint64_t* list, int n, int top) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         const int at = i * 64 + t;
-        const uint32_t key = static_cast<uint32_t>(list[at < n ? at : 0] >> 48);
+        const uint32_t key = static_cast<uint32_t>(list[at < n ? at : 0] >> (32 + kCoarse));
         v[i] = at < n ? key : 0;
     }
-    return border_value(nth_largest(v, top));
+    return border_value<kCoarse>(nth_largest<32 - kCoarse>(v, top));
 }
 template <class Tops>
 __device__ __forceinline__ float next_border(Tops& s, const uint64_t* list, int n, int top) {
@@ -221,33 +223,156 @@ __device__ __forceinline__ float next_border(Tops& s, const uint64_t* list, int 
     return s.border;
 }
 
-// The entries among which the row's `top` largest logits are, and how many they are.
-// s.packs holds the s.n_packs packs that reach `border`, as far as they fit.
-template <int B, int T, class Tops>
-__device__ __forceinline__ const uint64_t* settle(Tops& s, const Row& row, bool bf16, int top,
-                                                  float border, float largest, int* count) {
-    constexpr int kPacks = Tops::kPacks;
-    const int t = threadIdx.x;
-    int packs = static_cast<int>(s.n_packs < kPacks ? s.n_packs : kPacks);
-    bool many = s.n_packs > kPacks;
-    if (packs > kWide) border = next_border(s, s.packs, packs, top);
-    if (many) {  // once more, from memory
-        if (t == 0) s.n_packs = 0;
-        __syncthreads();
+// One of the three keys that cut lo .. hi into four, none at lo.
+__device__ __forceinline__ uint32_t cut(uint32_t lo, uint32_t hi, uint32_t i) {
+    const uint64_t at = lo + i * ((static_cast<uint64_t>(hi) - lo + 3) / 4);
+    return at < hi ? static_cast<uint32_t>(at) : hi;
+}
+
+// The row's `top` largest, from memory, where `border` is known to be reached by them:
+// two bits of the top-th largest's key a turn, then the logits above it, then as many of
+// those alike as there is room for, in order.
+template <int DT, int T, class Tops>
+__device__ __forceinline__ int search(Tops& s, const Row& row, int top, float border, float largest) {
+    constexpr int B = DT == ZERO_F32 ? 4 : 2, kShift = kExact<DT>, kWaves = T / 64;
+    constexpr bool bf16 = DT == ZERO_BF16;
+    const int t = threadIdx.x, wave = t / 64, lane = t % 64;
+    auto pack = [&](int p, float (&v)[8]) {
+        widen8<B>(load_aligned<B>(row.body + static_cast<int64_t>(p) * 8 * B), bf16, v);
+    };
+    uint32_t lo = order_key(border) >> kShift, hi = order_key(largest) >> kShift;
+#pragma unroll 1
+    for (int turn = 0; lo < hi; turn ^= 1) {
+        float at[3];
+        uint32_t reach[3] = {};
+#pragma unroll
+        for (int i = 0; i < 3; ++i) at[i] = border_value<kShift>(cut(lo, hi, i + 1));
 #pragma unroll 1
         for (int p = t; p < row.packs; p += T) {
-            float v[8], m;
-            widen8<B>(load_aligned<B>(row.body + static_cast<int64_t>(p) * 8 * B), bf16, v);
-            m = v[0];
+            float v[8];
+            pack(p, v);
 #pragma unroll
-            for (int k = 1; k < 8; ++k) m = fmaxf(m, v[k]);
+            for (int k = 0; k < 8; ++k) {
+#pragma unroll
+                for (int i = 0; i < 3; ++i) reach[i] += v[k] >= at[i];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            reach[i] += row.edge_x >= at[i];
+#pragma unroll
+            for (int d = 1; d < 64; d *= 2) reach[i] += __shfl_xor(reach[i], d);
+            if (lane == 0) s.reach[turn][i][wave] = reach[i];
+        }
+        __syncthreads();
+        uint32_t from = lo, to = hi;
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            uint32_t all = 0;
+            for (int w = 0; w < kWaves; ++w) all += s.reach[turn][i][w];
+            const uint32_t key = cut(lo, hi, i + 1);
+            if (all >= static_cast<uint32_t>(top)) from = key > from ? key : from;
+            else to = key - 1 < to ? key - 1 : to;
+        }
+        lo = from;
+        hi = to;
+    }
+    const float alike = exact_value<kShift>(lo);
+    if (t == 0) s.n_ranked = 0;
+    __syncthreads();
+#pragma unroll 1
+    for (int p = t; p < row.packs; p += T) {
+        float v[8];
+        pack(p, v);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (v[k] > alike) push(s.ranked, s.n_ranked, kRanked, entry(v[k], row.head + 8 * p + k));
+    }
+    if (row.edge_x > alike) push(s.ranked, s.n_ranked, kRanked, entry(row.edge_x, row.edge));
+    __syncthreads();
+    const int above = static_cast<int>(s.n_ranked), room = top - above;
+    const uint64_t below = (uint64_t{1} << lane) - 1;
+    // the head and the tail are the first wave's
+    const bool edge = row.edge_x == alike, first = row.edge < row.head;
+    int taken = 0;
+    auto put = [&](int at, int place) {
+        if (at < room) s.ranked[above + at] = entry(alike, place);
+    };
+    const uint64_t heads = __ballot(edge && first), tails = __ballot(edge && !first);
+    if (wave == 0) {
+        if (edge && first) put(__popcll(heads & below), row.edge);
+        if (lane == 0) s.n = __popcll(heads);
+    }
+    __syncthreads();
+    taken = static_cast<int>(s.n);
+#pragma unroll 1
+    for (int p0 = 0, turn = 0; p0 < row.packs && taken < room; p0 += T, turn ^= 1) {
+        float v[8];
+        const int p = p0 + t;
+        if (p < row.packs) pack(p, v);
+        int before = 0, all = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const uint64_t same = __ballot(p < row.packs && v[k] == alike);
+            before += __popcll(same & below);
+            all += __popcll(same);
+        }
+        if (lane == 0) s.reach[turn][0][wave] = static_cast<uint32_t>(all);
+        __syncthreads();
+        for (int w = 0; w < kWaves; ++w) {
+            const int n = static_cast<int>(s.reach[turn][0][w]);
+            before += w < wave ? n : 0;
+            all = w == 0 ? n : all + n;
+        }
+        if (p < row.packs) {
+            int at = taken + before;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (v[k] == alike) put(at++, row.head + 8 * p + k);
+        }
+        taken += all;
+    }
+    if (wave == 0) {
+        if (edge && !first) put(taken + __popcll(tails & below), row.edge);
+        if (lane == 0) s.n_packs = taken + __popcll(tails);
+    }
+    __syncthreads();
+    taken = static_cast<int>(s.n_packs);
+    return above + (taken < room ? taken : room);
+}
+
+// The entries among which the row's `top` largest logits are, and how many they are.
+// s.packs holds the s.n_packs packs that reach `border`, as far as they fit.
+template <int DT, int T, class Tops>
+__device__ __forceinline__ const uint64_t* settle(Tops& s, const Row& row, int top, float border,
+                                                  float largest, int* count) {
+    constexpr int kPacks = Tops::kPacks, B = DT == ZERO_F32 ? 4 : 2;
+    constexpr bool bf16 = DT == ZERO_BF16;
+    const int t = threadIdx.x;
+    int packs = static_cast<int>(s.n_packs);
+    if (__builtin_expect(packs > kPacks, 0)) {  // once more, from memory, with the whole row's border
+        auto pack_max = [&](int p) {
+            float v[8];
+            widen8<B>(load_aligned<B>(row.body + static_cast<int64_t>(p) * 8 * B), bf16, v);
+#pragma unroll
+            for (int k = 1; k < 8; ++k) v[0] = fmaxf(v[0], v[k]);
+            return v[0];
+        };
+        __syncthreads();
+        float lane_max = row.edge_x;
+#pragma unroll 1
+        for (int p = t; p < row.packs; p += T) lane_max = fmaxf(lane_max, pack_max(p));
+        border = first_border<T>(s, lane_max, top);
+#pragma unroll 1
+        for (int p = t; p < row.packs; p += T) {
+            const float m = pack_max(p);
             if (m >= border) push(s.packs, s.n_packs, kPacks, entry(m, p));
         }
         __syncthreads();
-        many = s.n_packs > kPacks;
         packs = static_cast<int>(s.n_packs);
     }
-    if (!many) {
+    if (__builtin_expect(packs <= kPacks, 1)) {
+        if (packs > kWide) border = next_border(s, s.packs, packs, top);
         for (int j = t; j < packs; j += T) {
             const uint64_t e = s.packs[j];
             if (!(entry_value(e) >= border)) continue;
@@ -262,10 +387,9 @@ __device__ __forceinline__ const uint64_t* settle(Tops& s, const Row& row, bool 
         if (row.edge_x >= border) push(s.collected, s.n, kCollected, entry(row.edge_x, row.edge));
         __syncthreads();
         const int n = static_cast<int>(s.n);
-        many = n > kCollected;
         *count = n;
-        if (n <= kWide) return s.collected;
-        if (!many) {
+        if (__builtin_expect(n <= kWide, 1)) return s.collected;
+        if (n <= kCollected) {
             border = next_border(s, s.collected, n, top);
             for (int j = t; j < n; j += T) {
                 const uint64_t e = s.collected[j];
@@ -273,35 +397,11 @@ __device__ __forceinline__ const uint64_t* settle(Tops& s, const Row& row, bool 
             }
             __syncthreads();
             *count = static_cast<int>(s.n_ranked);
-            many = *count > kRanked;
-            if (!many) return s.ranked;
+            if (*count <= kRanked) return s.ranked;
         }
     }
-    // bisection: the least entry of the `top` largest, which reach lo
-    uint64_t lo = entry(border, row.vocab), hi = entry(largest, 0);
-#pragma unroll 1
-    for (int turn = 0; lo < hi; turn ^= 1) {
-        const uint64_t mid = lo + (hi - lo) / 2 + ((hi - lo) & 1);
-        uint32_t reach = 0;
-        for_each<B, T>(row, bf16, [&](float v, int place) { reach += entry(v, place) >= mid; });
-#pragma unroll
-        for (int d = 1; d < 64; d *= 2) reach += __shfl_xor(reach, d);
-        if ((t & 63) == 0) s.reach[turn][t / 64] = reach;
-        __syncthreads();
-        reach = 0;
-        for (int w = 0; w < T / 64; ++w) reach += s.reach[turn][w];
-        if (reach >= static_cast<uint32_t>(top)) lo = mid;
-        else hi = mid - 1;
-    }
-    __syncthreads();
-    if (t == 0) s.n_ranked = 0;
-    __syncthreads();
-    for_each<B, T>(row, bf16, [&](float v, int place) {
-        const uint64_t e = entry(v, place);
-        if (e >= lo) push(s.ranked, s.n_ranked, kRanked, e);  // `top` of them
-    });
-    __syncthreads();
-    *count = static_cast<int>(s.n_ranked);
+    __syncthreads();  // before its counts are cleared
+    *count = search<DT, T>(s, row, top, border, largest);
     return s.ranked;
 }
 
@@ -458,8 +558,8 @@ __global__ __launch_bounds__(64 * kWaveRows, 8) void logprob_wave_kernel(const L
         if (bad) return;
         uint32_t v[R];
 #pragma unroll
-        for (int u = 0; u < R; ++u) v[u] = order_key(own[u]) >> 16;
-        const float border = border_value(nth_largest(v, a.top));
+        for (int u = 0; u < R; ++u) v[u] = order_key(own[u]) >> kCoarse;
+        const float border = border_value<kCoarse>(nth_largest<32 - kCoarse>(v, a.top));
         const uint64_t below = (uint64_t{1} << t) - 1;
         // f(value, place) for each logit of the wave's packs that reach the border, and
         // of its edges, by whole waves
@@ -476,31 +576,61 @@ __global__ __launch_bounds__(64 * kWaveRows, 8) void logprob_wave_kernel(const L
         };
         uint64_t* list = lists[wave];
         int n = 0;
-        auto collect = [&](uint64_t from) {
+        auto collect = [&](auto wanted) {
             n = 0;
             each([&](float x, int place) {
-                const uint64_t e = entry(x, place);
-                const uint64_t in = __ballot(x >= border && e >= from);
+                const uint64_t in = __ballot(wanted(x));
                 const int at = n + __popcll(in & below);
-                if ((in >> t & 1) && at < kWaveEntries) list[at] = e;
+                if ((in >> t & 1) && at < kWaveEntries) list[at] = entry(x, place);
                 n += __popcll(in);
             });
         };
-        collect(0);
+        collect([&](float x) { return x >= border; });
         if (n > kWaveEntries) {
-            // bisection: the least entry of the `top` largest, which reach lo
-            uint64_t lo = entry(border, row.vocab), hi = entry(st.m, 0);
+            // the exact value of the top-th largest, bit by bit; the logits above it;
+            // those alike in order, as many as there is room for
+            constexpr int kShift = kExact<DT>;
+            uint32_t lo = order_key(border) >> kShift, hi = order_key(st.m) >> kShift;
 #pragma unroll 1
             while (lo < hi) {
-                const uint64_t mid = lo + (hi - lo) / 2 + ((hi - lo) & 1);
+                const uint32_t mid = lo + (hi - lo) / 2 + ((hi - lo) & 1);
+                const float at = border_value<kShift>(mid);
                 int reach = 0;
-                each([&](float x, int place) {
-                    reach += __popcll(__ballot(x >= border && entry(x, place) >= mid));
-                });
+                each([&](float x, int) { reach += __popcll(__ballot(x >= at)); });
                 if (reach >= a.top) lo = mid;
                 else hi = mid - 1;
             }
-            collect(lo);
+            const float alike = exact_value<kShift>(lo);
+            collect([&](float x) { return x > alike; });
+            auto ties = [&](float x, int place, int before) {
+                if (x == alike && n + before < a.top) list[n + before] = entry(x, place);
+            };
+            const uint64_t edges = __ballot(row.edge_x == alike);
+            const uint64_t heads = edges & ((uint64_t{1} << row.head) - 1), tails = edges & ~heads;
+            if (t < row.head) ties(row.edge_x, row.edge, __popcll(heads & below));
+            n += __popcll(heads);
+#pragma unroll
+            for (int u = 0; u < R; ++u) {
+                if (n >= a.top) continue;
+                float x[8];
+                widen8<B>(r[u], bf16, x);
+                int before = 0, all = 0;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const uint64_t same = __ballot(x[k] == alike);
+                    before += __popcll(same & below);
+                    all += __popcll(same);
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    ties(x[k], row.head + 8 * (u * 64 + t) + k, before);
+                    before += x[k] == alike;
+                }
+                n += all;
+            }
+            if (t >= row.head) ties(row.edge_x, row.edge, __popcll(tails & below));
+            n += __popcll(tails);
+            n = n < a.top ? n : a.top;
         }
         // the wave's writes to its list before its reads of it
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -515,7 +645,7 @@ __global__ __launch_bounds__(64 * kWaveRows, 8) void logprob_wave_kernel(const L
 // T lanes per row, which take R packs of eight each at a time; without STREAM that is
 // the whole row.
 template <int DT, int T, int R, bool STREAM, bool TOP>
-__global__ __launch_bounds__(T, 8) void logprob_kernel(const LogprobArgs a, int64_t first) {
+__global__ __launch_bounds__(T, STREAM && TOP && T == 256 ? 5 : 8) void logprob_kernel(const LogprobArgs a, int64_t first) {
     constexpr int B = DT == ZERO_F32 ? 4 : 2;
     constexpr bool bf16 = DT == ZERO_BF16;
     constexpr int kWaves = T / 64;
@@ -577,7 +707,7 @@ __global__ __launch_bounds__(T, 8) void logprob_kernel(const LogprobArgs a, int6
     if constexpr (TOP) {
         if (bad) return;
         int n;
-        const uint64_t* entries = settle<B, T>(s, row, bf16, a.top, border, st.m, &n);
+        const uint64_t* entries = settle<DT, T>(s, row, a.top, border, st.m, &n);
         put_tops<DT, T>(entries, n, a, row_at);
     }
 }
@@ -598,10 +728,13 @@ hipError_t logprob_size(const LogprobArgs& a, hipStream_t stream) {
                                return hipGetLastError();
                            });
     if (a.vocab <= 256 * 4 * 8) return run(logprob_kernel<DT, 256, 4, false, TOP>, 256);
+    // Many rows go by in small workgroups, so that others load while one settles its
+    // alternatives; few rows have a CU each to themselves.  fp16, with 64 alternatives,
+    // by 256, 512 and 1,024 lanes: 4096 x 131072 226, 233 and 266 us, 8192 x 20000 116,
+    // 135 and 207, 1024 x 131072 73, 68 and 77, 256 x 131072 46, 36 and 33.
+    if (a.rows >= 2048) return run(logprob_kernel<DT, 256, 4, true, TOP>, 256);
+    if (a.rows >= 512) return run(logprob_kernel<DT, 512, 4, true, TOP>, 512);
     if (a.vocab <= 512 * 4 * 8) return run(logprob_kernel<DT, 512, 4, false, TOP>, 512);
-    if constexpr (!TOP && DT != ZERO_F32) {
-        if (a.vocab <= 512 * 8 * 8) return run(logprob_kernel<DT, 512, 8, false, TOP>, 512);
-    }
     if (a.vocab <= 1024 * 4 * 8) return run(logprob_kernel<DT, 1024, 4, false, TOP>, 1024);
     return run(logprob_kernel<DT, 1024, 4, true, TOP>, 1024);
 }

@@ -150,21 +150,48 @@ def test_single_rows_of_wider_matrices():
 # border.
 @pytest.mark.parametrize("dtype", [F16, BF16, F32])
 @pytest.mark.parametrize("vocab", [2000, 8192, 16001, 40000, 131072])
-@pytest.mark.parametrize("rows", ["rising", "falling", "alike", "few values", "saw"])
+@pytest.mark.parametrize("rows", ["rising", "falling", "alike", "few values", "saw", "masked"])
 def test_alternatives_of_rows_with_many_on_the_border(rows, vocab, dtype):
     device()
     i = torch.arange(vocab, device="cuda", dtype=torch.float64)
     x = {"rising": i / vocab, "falling": 1 - i / vocab, "alike": 0 * i + 2.5, "few values": i % 3,
-         "saw": (i * 7919 % 4096) / 4096}[rows]
-    logits = torch.stack([x, x.flip(0), x - 5, x * 1e4]).to(dtype)
-    for top in (1, 20, 128):
-        index = torch.empty(4, top, dtype=torch.int32, device="cuda")
-        value = torch.empty(4, top, dtype=dtype, device="cuda")
-        zs.zero_logprob(logits, None, None, top_index=index, top_logit=value)
-        # a stable sort of the negatives: ties by the lowest place
-        order = torch.sort(-logits.double(), dim=1, stable=True).indices[:, :top]
-        assert torch.equal(index.long(), order)
-        assert torch.equal(value, logits.gather(1, order))
+         "saw": (i * 7919 % 4096) / 4096,
+         "masked": torch.where(i % 1111 == 7, i / vocab, torch.finfo(dtype).min)}[rows]
+    few = torch.stack([x, x.flip(0), x - 5, x * 1e4]).to(dtype).clamp_min(torch.finfo(dtype).min)
+    # a stable sort of the negatives: ties by the lowest place
+    order = torch.sort(-few.double(), dim=1, stable=True).indices[:, :128]
+    for times in (1, 128, 512):  # as few, more and many rows
+        logits = few.repeat(times, 1)
+        for top in (1, 20, 128):
+            index = torch.empty(4 * times, top, dtype=torch.int32, device="cuda")
+            value = torch.empty(4 * times, top, dtype=dtype, device="cuda")
+            zs.zero_logprob(logits, None, None, top_index=index, top_logit=value)
+            want = order[:, :top].repeat(times, 1)
+            assert torch.equal(index.long(), want)
+            assert torch.equal(value, logits.gather(1, want))
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+@pytest.mark.parametrize("vocab", [8193, 16385, 32009, 70001])
+@pytest.mark.parametrize("rows", [511, 512, 2047, 2048])
+def test_log_probabilities_of_many_rows(rows, vocab, dtype):
+    device()
+    logits = 3 * _randn(1, rows, vocab, dtype=dtype)
+    logits[5, 9:] = -math.inf
+    logits[6, 77] = math.nan
+    ids = torch.randint(-1, vocab, (rows,), generator=_gen(2), device="cuda")
+    ids[7], ids[8] = -1, vocab
+    out = [torch.full((rows,), 7.0, device="cuda") for _ in range(3)]
+    index = torch.empty(rows, 20, dtype=torch.int32, device="cuda")
+    value = torch.empty(rows, 20, dtype=dtype, device="cuda")
+    zs.zero_logprob(logits, ids, out[0], entropy=out[1], lse=out[2], top_index=index,
+                    top_logit=value)
+    for cut in torch.arange(rows, device="cuda").split(256):
+        want, tol = ref.logprob(logits[cut], ids[cut], 1.0, 20)
+        for got, w, t in zip(out, want, tol):
+            ref.assert_close(got[cut], w, t + ref.half_step(F32, w.nan_to_num(0, 0, 0)), "sums")
+        assert torch.equal(index[cut], want[3])
+        assert torch.equal(value[cut].float().nan_to_num(9e9), want[4].float().nan_to_num(9e9))
 
 
 # ---- more workgroups than a launch has ------------------------------------------------
