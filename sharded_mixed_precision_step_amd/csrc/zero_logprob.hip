@@ -179,14 +179,13 @@ __device__ __forceinline__ float exact_value(uint32_t key) {
     return key_value(key << SHIFT | (key >> (31 - SHIFT) ? 0u : (1u << SHIFT) - 1));
 }
 
-// A border that the row's `top` largest reach, from the lanes' maxima.
+// A border that the row's `top` largest reach, from the lanes' maxima so far.
 template <int T, class Tops>
-__device__ __forceinline__ float first_border(Tops& s, float lane_max, int top) {
+__device__ __forceinline__ float maxima_border(Tops& s, float lane_max, int top) {
     const int t = threadIdx.x;
 #pragma unroll
     for (int d = 1; d < T / kGroups; d *= 2) lane_max = fmaxf(lane_max, __shfl_xor(lane_max, d));
     if (t % (T / kGroups) == 0) s.group_max[t / (T / kGroups)] = lane_max;
-    if (t == 0) s.n_packs = s.n = s.n_ranked = 0;
     __syncthreads();
     if (t < 64) {
         uint32_t v[kGroups / 64];
@@ -198,6 +197,12 @@ __device__ __forceinline__ float first_border(Tops& s, float lane_max, int top) 
     }
     __syncthreads();
     return s.border;
+}
+
+template <int T, class Tops>
+__device__ __forceinline__ float first_border(Tops& s, float lane_max, int top) {
+    if (threadIdx.x == 0) s.n_packs = s.n = s.n_ranked = 0;
+    return maxima_border<T>(s, lane_max, top);
 }
 
 // A closer one, from a list's first 64 N entries (`top` at least).
@@ -524,7 +529,7 @@ __device__ __forceinline__ bool put_row(const LogprobArgs& a, int64_t row_at, in
 // that reach it take their places in LDS by ballots.
 
 constexpr int kWavePacks = 4, kWaveRows = 4;
-constexpr int kWaveEntries = 512;
+constexpr int kWaveEntries = 256;
 
 template <int DT, bool TOP>
 __global__ __launch_bounds__(64 * kWaveRows, 8) void logprob_wave_kernel(const LogprobArgs a,
@@ -663,7 +668,7 @@ __global__ __launch_bounds__(T, STREAM && TOP && T == 256 ? 5 : 8) void logprob_
     }
     const Row row = row_of<DT>(a, row_at, t);
     const float at_id = a.logp && id < row.vocab ? load1(row.x, id, DT) : 0.0f;
-    float border = 0.0f, own[R];
+    float border = 0.0f, lane_max = row.edge_x, own[R];
     auto note = [&](int p0) {
 #pragma unroll
         for (int u = 0; u < R; ++u)
@@ -685,17 +690,27 @@ __global__ __launch_bounds__(T, STREAM && TOP && T == 256 ? 5 : 8) void logprob_
         }
     }
     if constexpr (TOP) {
-        float lane_max = row.edge_x;
 #pragma unroll
         for (int u = 0; u < R; ++u) lane_max = fmaxf(lane_max, own[u]);
         border = first_border<T>(s, lane_max, a.top);
         note(0);
     }
     if constexpr (STREAM) {
+        // The border follows the maxima when four times as much of the row has gone by, so
+        // that the list has room for rows of any length.
+        int closer_at = 4 * R * T;
         for (int p0 = R * T; p0 < row.packs; p0 += R * T) {
             load_packs<DT, T, R>(row, p0, t, r);
+            if (TOP && p0 == closer_at) {
+                border = maxima_border<T>(s, lane_max, a.top);
+                closer_at *= 4;
+            }
             take<B, R>(st, r, bf16, c, own);
-            if constexpr (TOP) note(p0);
+            if constexpr (TOP) {
+#pragma unroll
+                for (int u = 0; u < R; ++u) lane_max = fmaxf(lane_max, own[u]);
+                note(p0);
+            }
         }
     }
     take_edge(st, row, c);
