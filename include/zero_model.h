@@ -73,7 +73,8 @@ int64_t zero_embed_backward_workspace(int64_t tokens, int64_t vocab, int64_t col
 
 /*
  * zero_embed_backward -- dtable[v] = scale * sum of dy[r] over the tokens r with
- * ids[r] == v, added in fp32 in an order fixed by the ids, rounded once.
+ * ids[r] == v, added in fp32 in an order fixed by the ids and sizes, rounded
+ * once.
  *
  *   dy, dy_dtype, ld_dy      [tokens][cols], 0 <= tokens <= ZERO_EMBED_MAX_TOKENS
  *   ids, id_bytes            [tokens]; tokens whose id is negative, vocab or above
@@ -228,6 +229,10 @@ int zero_act_backward(const void* dy, int32_t dy_dtype, int64_t ld_dy, const voi
  *   - A row with an id >= vocab, a NaN or +inf among its logits, or no logit above
  *     -inf gives NaN for logp, entropy and lse, and NaN at place 0 for each
  *     alternative, which zero_distill turns into NaN.
+ *   - An lse beyond fp32's range is infinite (logits / temperature of 3e38), logp and
+ *     entropy are taken without it.  top_logit has no negative zeros.
+ * The order of a row's sums follows from rows, vocab and dtype, so that the same row
+ * among few and among many may differ in its last bits.
  * Returns ZERO_OK, ZERO_EINVAL, ZERO_EALIGN, ZERO_ERANGE (top) or ZERO_EHIP.
  */
 int zero_logprob(const void* logits, int32_t dtype, int64_t ld, int64_t rows, int64_t vocab,

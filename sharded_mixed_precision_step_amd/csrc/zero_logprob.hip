@@ -12,6 +12,10 @@
 // many come before each of their logits, by value and place, orders them.  Where too many
 // lie on the border, as in long ties, the row is read again for the exact value of the
 // top-th largest, and its ties are taken in the order of their places.
+//
+// Bound by HBM with many rows: 4096 x 131072 fp16 196 us, 222 with 64 alternatives (5.5
+// and 4.8 TB/s); and by the row's chain (load, sums, borders, places) with few: 37 x
+// 32001 bf16 with 20 alternatives 10 us.
 #include "zero_device.h"
 #include "zero_model_internal.h"
 
@@ -526,7 +530,8 @@ __device__ __forceinline__ bool put_row(const LogprobArgs& a, int64_t row_at, in
 // ---- a wave per row ----------------------------------------------------------
 // Rows of up to 2,048 stay in a wave's registers, four packs a lane, and need no
 // barrier.  The top-th largest of the 256 packs' maxima is the border; the logits
-// that reach it take their places in LDS by ballots.
+// that reach it take their places in LDS by ballots.  65536 x 256 fp16 31 us, 75 with 20
+// alternatives (a workgroup per row 196 and 275).
 
 constexpr int kWavePacks = 4, kWaveRows = 4;
 constexpr int kWaveEntries = 256;
@@ -648,7 +653,8 @@ __global__ __launch_bounds__(64 * kWaveRows, 8) void logprob_wave_kernel(const L
 // ---- a workgroup per row -------------------------------------------------------
 
 // T lanes per row, which take R packs of eight each at a time; without STREAM that is
-// the whole row.
+// the whole row.  Bounded to 64 registers (eight waves a SIMD): a kernel of more scalar
+// registers than that allows held one workgroup of 1,024 a CU instead of two.
 template <int DT, int T, int R, bool STREAM, bool TOP>
 __global__ __launch_bounds__(T, STREAM && TOP && T == 256 ? 5 : 8) void logprob_kernel(const LogprobArgs a, int64_t first) {
     constexpr int B = DT == ZERO_F32 ? 4 : 2;
@@ -764,7 +770,7 @@ hipError_t logprob_type(const LogprobArgs& a, hipStream_t stream) {
 constexpr int kGradLanes = 256, kGradPacks = 4;
 
 // 2^shift lanes to a row, U packs of eight a lane.  p_v and log p_v come from lse, so
-// a row's slices are independent.
+// a row's slices are independent.  Bound by HBM: 2048 x 50001 fp16 74 us, 5.5 TB/s.
 template <int DT, int U>
 __global__ __launch_bounds__(kGradLanes) void logprob_backward_kernel(const LogprobBackwardArgs a,
                                                                       int64_t first, int shift,
@@ -812,8 +818,8 @@ __global__ __launch_bounds__(kGradLanes) void logprob_backward_kernel(const Logp
     }
 }
 
-// Lanes per row, as a power of two: what its packs need, up to a workgroup, with four
-// packs a lane beyond that.
+// Lanes per row, as a power of two: what its packs need, up to a workgroup (a workgroup
+// whatever the row: 65536 x 256 fp16 190 us, 15 so), with four packs a lane beyond that.
 int grad_shift(int64_t vocab) {
     int shift = 0;
     while (shift < 8 && (int64_t{8} << shift) < vocab) ++shift;
