@@ -70,6 +70,27 @@ def test_embedding_gradient_where_its_ways_change(tokens, vocab, cols, gap):
     assert torch.equal(_backward(dy, ids, vocab, old, gap), want + old)
 
 
+@pytest.mark.parametrize("dy_dtype,dt_dtype", [(F32, F16), (F16, BF16), (BF16, F16), (F32, F32)])
+@pytest.mark.parametrize("tokens,cols", [(300, 20), (3000, 20), (530000, 16)])
+def test_embedding_gradient_types_where_its_ways_change(tokens, cols, dy_dtype, dt_dtype):
+    """Whole numbers: the fp32 sums are exact, and rounded once."""
+    device()
+    vocab = 700
+    ids = torch.randint(-9, vocab // 2, (tokens,), device="cuda", generator=_gen(1))
+    dy = _whole(2, tokens, cols).to(dy_dtype)
+    want = torch.zeros(vocab, cols, device="cuda")
+    want.index_add_(0, ids[ids >= 0], dy[ids >= 0].float())
+    work = torch.empty(zs.zero_embed_backward_workspace(tokens, vocab, cols), dtype=torch.uint8,
+                       device="cuda")
+    d = torch.full((vocab, cols), 7.0, dtype=dt_dtype, device="cuda")
+    zs.zero_embed_backward(dy, ids, d, work)
+    assert torch.equal(d, want.to(dt_dtype))
+    d = _whole(3, vocab, cols).to(dt_dtype)
+    old = d.float().clone()
+    zs.zero_embed_backward(dy, ids, d, work, accumulate=True)
+    assert torch.equal(d, (want + old).to(dt_dtype))
+
+
 @pytest.mark.parametrize("tokens", [512, 513, 16384, 16385, 300000])
 def test_embedding_gradient_of_one_token_over_and_over(tokens):
     device()
@@ -192,6 +213,23 @@ def test_log_probabilities_of_many_rows(rows, vocab, dtype):
             ref.assert_close(got[cut], w, t + ref.half_step(F32, w.nan_to_num(0, 0, 0)), "sums")
         assert torch.equal(index[cut], want[3])
         assert torch.equal(value[cut].float().nan_to_num(9e9), want[4].float().nan_to_num(9e9))
+
+
+@pytest.mark.parametrize("times,vocab", [(1, 4000003), (120, 600011), (410, 262145)])
+def test_alternatives_of_long_rows(times, vocab):
+    """The border moves several times on its way."""
+    device()
+    few = _randn(1, 5, vocab, dtype=F16)
+    few[1] = few[1].sort().values
+    few[2] = few[2].sort(descending=True).values
+    few[3, 100:-100] = -math.inf
+    few[4] = (few[4] * 2).round()
+    order = torch.sort(-few.float(), dim=1, stable=True).indices[:, :128]
+    logits, want = few.repeat(times, 1), order.repeat(times, 1)
+    index = torch.empty(5 * times, 128, dtype=torch.int32, device="cuda")
+    value = torch.empty(5 * times, 128, dtype=F16, device="cuda")
+    zs.zero_logprob(logits, None, None, top_index=index, top_logit=value)
+    assert torch.equal(index.long(), want) and torch.equal(value, logits.gather(1, want))
 
 
 # ---- more workgroups than a launch has ------------------------------------------------
