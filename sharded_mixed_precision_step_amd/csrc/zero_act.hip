@@ -29,9 +29,14 @@ __device__ __forceinline__ Slope sigmoid(float v) {
     return v < 0.0f ? Slope{small, big} : Slope{big, small};
 }
 
-template <int KIND>
+// DERIVED: the derivative is asked for too.
+template <int KIND, bool DERIVED>
 __device__ __forceinline__ Slope slope(float g) {
-    if constexpr (KIND == ZERO_SILU) {
+    if constexpr (KIND == ZERO_SILU && !DERIVED) {
+        // exp(-g) may overflow, and below -87, where f is under 1e-36, s is 0.  (By the
+        // form with both ends 8192 x 14336 162 us, 158 so.)
+        return {__builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * g)), 0.0f};
+    } else if constexpr (KIND == ZERO_SILU) {
         const Slope p = sigmoid(g);
         return {p.s, p.s * p.d};
     } else if constexpr (KIND == ZERO_GELU) {
@@ -119,7 +124,7 @@ __global__ __launch_bounds__(kLanes) void act_kernel(const ActArgs a, int64_t fi
     if (!a.y && !a.q) return;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-        g[k] = g[k] * slope<KIND>(g[k]).s;
+        g[k] = g[k] * slope<KIND, false>(g[k]).s;
         if constexpr (UP) g[k] *= u[k];
     }
     if (a.y) store8(a.y, p.row * a.ld_y + p.c, p.n, a.y_dtype, g);
@@ -170,7 +175,7 @@ __global__ __launch_bounds__(kLanes) void act_backward_kernel(const ActBackwardA
     float dup[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-        const Slope v = slope<KIND>(g[k]);
+        const Slope v = slope<KIND, true>(g[k]);
         float f = g[k] * v.s, d = dy[k] * __builtin_fmaf(g[k], v.d, v.s);
         if constexpr (UP) {
             dup[k] = dy[k] * f;
