@@ -64,8 +64,10 @@ __global__ __launch_bounds__(kLanes) void embed_kernel(const EmbedArgs a, int64_
 // ---- sort ------------------------------------------------------------------
 
 constexpr int kDigit = 9, kBins = 1 << kDigit;
-constexpr int kSortRounds = 16;
-constexpr int kSortItems = kLanes * kSortRounds;  // items per workgroup
+// Items of a lane: few, so that there are workgroups for every CU, up to 131,072 tokens
+// (65536 of 32000 x 8 fp16 55 us with 16, 43 with 4; 16777216 of 50000 x 8 1.82 ms and
+// 2.05, since each workgroup's counts are read again).
+__host__ __device__ inline int sort_rounds(int64_t tokens) { return tokens <= 131072 ? 4 : 16; }
 
 // A token's key: its row of the table, or vocab (behind all rows) if it has none.
 __device__ __forceinline__ uint32_t sort_key(int64_t id, int64_t vocab) {
@@ -150,15 +152,16 @@ __device__ __forceinline__ void rank_items(const uint32_t (&key)[N], int shift, 
 }
 
 // counts[block][digit]
+template <int ROUNDS>
 __global__ __launch_bounds__(kLanes) void sort_count_kernel(const SortPass a) {
     __shared__ uint32_t bins[kBins];
     for (int d = threadIdx.x; d < kBins; d += kLanes) bins[d] = 0;
-    const int64_t i0 = static_cast<int64_t>(blockIdx.x) * kSortItems + threadIdx.x;
-    uint32_t key[kSortRounds];
-    load_keys<kSortRounds, kLanes>(a, i0, key);
+    const int64_t i0 = static_cast<int64_t>(blockIdx.x) * (kLanes * ROUNDS) + threadIdx.x;
+    uint32_t key[ROUNDS];
+    load_keys<ROUNDS, kLanes>(a, i0, key);
     __syncthreads();
 #pragma unroll
-    for (int r = 0; r < kSortRounds; ++r)
+    for (int r = 0; r < ROUNDS; ++r)
         if (i0 + r * kLanes < a.tokens) atomicAdd(&bins[key[r] >> a.shift & (kBins - 1)], 1u);
     __syncthreads();
     for (int d = threadIdx.x; d < kBins; d += kLanes)
@@ -196,6 +199,7 @@ __global__ __launch_bounds__(64 * kScanWaves) void sort_scan_kernel(uint32_t* co
 
 // Places the items behind those of lower digits, of earlier blocks, waves and
 // rounds, and of lower lanes.
+template <int ROUNDS>
 __global__ __launch_bounds__(kLanes) void sort_scatter_kernel(const SortPass a) {
     constexpr int kWaves = kLanes / 64, kPer = kBins / kLanes;  // digits a lane adds up
     __shared__ unsigned long long peers[kWaves][kBins];
@@ -206,11 +210,11 @@ __global__ __launch_bounds__(kLanes) void sort_scatter_kernel(const SortPass a) 
         peers[0][d] = 0;
         bins[0][d] = 0;
     }
-    const int64_t i0 = static_cast<int64_t>(blockIdx.x) * kSortItems + wave * 64 * kSortRounds;
-    uint32_t key[kSortRounds], rank[kSortRounds], place[kSortRounds];
-    load_keys<kSortRounds, 64>(a, i0 + lane, key);
+    const int64_t i0 = static_cast<int64_t>(blockIdx.x) * (kLanes * ROUNDS) + wave * 64 * ROUNDS;
+    uint32_t key[ROUNDS], rank[ROUNDS], place[ROUNDS];
+    load_keys<ROUNDS, 64>(a, i0 + lane, key);
 #pragma unroll
-    for (int r = 0; r < kSortRounds; ++r) {
+    for (int r = 0; r < ROUNDS; ++r) {
         const int64_t i = i0 + r * 64 + lane;
         place[r] = a.order_in ? a.order_in[i < a.tokens ? i : a.tokens - 1]
                               : static_cast<uint32_t>(i);
@@ -236,8 +240,8 @@ __global__ __launch_bounds__(kLanes) void sort_scatter_kernel(const SortPass a) 
     }
     __syncthreads();
     const int64_t left = a.tokens - i0;
-    rank_items(key, a.shift, kSortRounds, static_cast<int>(left < 0 ? 0 : left < 64 * kSortRounds
-                                                               ? left : 64 * kSortRounds),
+    rank_items(key, a.shift, ROUNDS, static_cast<int>(left < 0 ? 0 : left < 64 * ROUNDS
+                                                               ? left : 64 * ROUNDS),
                peers[wave], bins[wave], rank);
     uint32_t total = 0;
 #pragma unroll
@@ -265,7 +269,7 @@ __global__ __launch_bounds__(kLanes) void sort_scatter_kernel(const SortPass a) 
     }
     __syncthreads();
 #pragma unroll
-    for (int r = 0; r < kSortRounds; ++r) {
+    for (int r = 0; r < ROUNDS; ++r) {
         if (i0 + r * 64 + lane >= a.tokens) continue;
         const uint32_t at = bins[wave][key[r] >> a.shift & (kBins - 1)] + rank[r];
         a.keys_out[at] = key[r];
@@ -277,7 +281,7 @@ __global__ __launch_bounds__(kLanes) void sort_scatter_kernel(const SortPass a) 
 
 constexpr int kStartLanes = 1024, kStartWaves = kStartLanes / 64;
 constexpr int kSmallRounds = 16;
-constexpr int64_t kSmall = kStartLanes * kSmallRounds;  // tokens that one workgroup sorts
+constexpr int64_t kSmall = kStartLanes * kSmallRounds;  // tokens that one workgroup may sort
 
 struct Fill {
     void* p;
@@ -306,7 +310,7 @@ __device__ __forceinline__ void fill_zeros(const Fill& f, int64_t tile) {
 // All passes over up to kSmall tokens by one workgroup, the items in registers
 // during a pass and in LDS between passes, where the peers' bits are during one: 15 us
 // for 4096 tokens, 20 for 8192, 32 for 16384, mostly behind the zeros.  (By several
-// workgroups, two launches a pass, 65536 take 29 us, and nothing else goes on meanwhile.)
+// workgroups, two launches a pass, it takes 17 us, and nothing else goes on meanwhile.)
 constexpr int kPeersWords = kStartWaves * kBins * 2, kBinsWords = kStartWaves * kBins;
 __host__ __device__ inline int small_words(int rounds) {
     const int items = rounds * kStartLanes * 6 / 4;
@@ -780,7 +784,7 @@ EmbedWorkspace embed_workspace(int64_t tokens, int64_t cols) {
         at = up16(at + 4 * tokens);
     }
     w.counts = at;
-    at = up16(at + 4 * kBins * (1 + ceil_div(tokens, kSortItems)));
+    at = up16(at + 4 * kBins * (1 + ceil_div(tokens, kLanes * sort_rounds(tokens))));
     w.parts = at;
     w.bytes = at + 4 * 2 * pieces(tokens, cols) * cols;
     return w;
@@ -838,22 +842,32 @@ namespace {
 // The whole sort of many tokens; the last pass's keys and order.
 hipError_t sort_many(SortPass p, uint32_t* const (&keys)[2], uint32_t* const (&order)[2],
                      hipStream_t stream, Sorted* s) {
-    const uint32_t grid = static_cast<uint32_t>(ceil_div(p.tokens, kSortItems));
+    const int rounds = sort_rounds(p.tokens);
+    const uint32_t grid = static_cast<uint32_t>(ceil_div(p.tokens, kLanes * rounds));
     int to = 0;
     p.scanned = grid > kUnscanned;
     for (p.shift = 0; p.vocab >> p.shift; p.shift += kDigit, to ^= 1) {
         p.keys_out = keys[to];
         p.order_out = order[to];
-        sort_count_kernel<<<grid, kLanes, 0, stream>>>(p);
+        if (rounds == 4) sort_count_kernel<4><<<grid, kLanes, 0, stream>>>(p);
+        else sort_count_kernel<16><<<grid, kLanes, 0, stream>>>(p);
         if (p.scanned)
             sort_scan_kernel<<<kBins / 64, 64 * kScanWaves, 0, stream>>>(p.counts, grid);
-        sort_scatter_kernel<<<grid, kLanes, 0, stream>>>(p);
+        if (rounds == 4) sort_scatter_kernel<4><<<grid, kLanes, 0, stream>>>(p);
+        else sort_scatter_kernel<16><<<grid, kLanes, 0, stream>>>(p);
         p.keys_in = keys[to];
         p.order_in = order[to];
     }
     s->keys = p.keys_in;
     s->order = p.order_in;
     return hipGetLastError();
+}
+
+// Whether one workgroup sorts beside the zeros.  By several, in launches of their own, it
+// takes about 17 us whatever the number, so that beyond 8,192 tokens the zeros have to
+// hide what one takes more, 11 KB a token (16384 of 5000 x 64 fp16 45 us by one, 34 so).
+bool one_sorts(int64_t tokens, int64_t zeros) {
+    return tokens <= 8192 || (tokens <= kSmall && zeros / 11000 >= tokens - 8192);
 }
 
 template <int TB>
@@ -922,7 +936,7 @@ hipError_t launch_embed_backward(const EmbedBackwardArgs& a, hipStream_t stream)
         s.length = piece_length(a.tokens, a.cols);
         p.tokens = a.tokens; p.vocab = a.vocab; p.id_bytes = a.id_bytes;
         s.parts = reinterpret_cast<float*>(a.workspace + w.parts);
-        if (a.tokens <= kSmall) {
+        if (one_sorts(a.tokens, a.accumulate ? 0 : 2 * a.vocab * halves(a.cols, a.dt_dtype))) {
             while (a.vocab >> (passes * kDigit)) ++passes;
             lds = 4 * static_cast<size_t>(
                           small_words(static_cast<int>(ceil_div(a.tokens, kStartLanes))));
