@@ -2,7 +2,7 @@
 //
 // Elementwise but for the largest magnitude of each block of 128, which is 16
 // neighbouring lanes' (eight elements a lane), and bound by HBM: a lane holds one
-// pack of each array.  8192 x 14336 fp16 gated, e4m3 output and checkpoints: 154 to 159
+// pack of each array.  8192 x 14336 fp16 gated, e4m3 output and checkpoints: 152 to 159
 // us, 5.2 to 5.4 TB/s; its gradient with y once more 203 us, 5.8 TB/s.  1003 x 5001 bf16,
 // GELU: 8.8 us for what 5.3 would carry, two rounds of waves and rows at odd addresses.
 #include "zero_device.h"
