@@ -52,7 +52,8 @@ def _backward(dy, ids, vocab, old=None, gap=0):
                                                (2000, 1 << 18, 16), (20000, (1 << 18) - 1, 8),
                                                (20000, (1 << 18) + 1, 8), (16384, 1 << 20, 8),
                                                (530000, 3000, 8), (530000, 1 << 19, 8),
-                                               (66000, 100, 4104)])
+                                               (66000, 100, 4104), (9000, 30000, 80),
+                                               (12345, 40000, 300), (16384, 60000, 400)])
 def test_embedding_gradient_where_its_ways_change(tokens, vocab, cols, gap):
     device()
     print(f"case: embed backward {tokens} of {vocab}x{cols} gap {gap}", flush=True)
