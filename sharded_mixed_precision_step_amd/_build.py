@@ -171,6 +171,7 @@ def build(verbose: bool = False) -> str:
             _run_all([*compiles, marshal_command(marshal)], verbose)
             _run_all([cmd for _, _, cmd in links], verbose)
             for lib, tmp in (*((lib, tmp) for lib, tmp, _ in links), (MARSHAL_LIB, marshal)):
+                os.chmod(tmp, 0o755)  # g++ leaves the temporary file's mode, its owner's alone
                 os.replace(tmp, lib)
         finally:
             for tmp in temps:
