@@ -116,6 +116,12 @@ def kernel_digest() -> str:
     return h.hexdigest()
 
 
+def _source(cmd) -> str:
+    """The source that a command compiles, or the file that it links."""
+    sources = [a for a in cmd if a.endswith((".hip", ".cpp"))]
+    return sources[0] if sources else cmd[cmd.index("-o") + 1]
+
+
 def _run_all(commands, verbose: bool) -> None:
     """Run the commands side by side; raise with the output of those that fail."""
     procs = []
@@ -129,7 +135,8 @@ def _run_all(commands, verbose: bool) -> None:
         for cmd, proc in procs:
             out, err = proc.communicate()
             if proc.returncode != 0:
-                errors.append(f"hipcc failed ({proc.returncode}) for {cmd[-1]}:\n{out}\n{err}")
+                errors.append(f"{os.path.basename(cmd[0])} failed ({proc.returncode}) for "
+                              f"{_source(cmd)}:\n{out}\n{err}")
             elif verbose and err.strip():
                 print(err, flush=True)
         if errors:
