@@ -4,7 +4,8 @@ Argument marshalling only: tensors become raw device pointers, the current
 torch stream becomes a hipStream_t, and every call goes straight to the C ABI
 declared in include/zero_step.h.  All arithmetic of the step runs in the HIP
 kernels; nothing here computes on data.  If the library is missing the import
-fails loudly: there is no fallback path.
+fails loudly: there is no fallback path.  (The host library _marshal only
+shortens the way into calls of it; without one they go through ctypes.)
 
 torch is imported before the library is loaded so that the process holds a
 single HIP runtime (torch's libamdhip64.so.7 satisfies the library's
@@ -14,7 +15,10 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import importlib.util
 import os
+import sys
+import warnings
 from typing import Optional, Sequence
 
 import torch  # noqa: F401  (loads the HIP runtime first; see module docstring)
@@ -153,6 +157,26 @@ def _load() -> ctypes.CDLL:
 
 
 lib = _load()
+
+
+def _load_marshal():
+    """The binding's host library built for this Python and this torch, or None."""
+    name, path = f"{__name__}._marshal", _build.MARSHAL_LIB
+    try:
+        if not os.path.exists(path):
+            raise ImportError(f"{path} is not built")
+        spec = importlib.util.spec_from_file_location(name, path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+    except ImportError as e:
+        warnings.warn(f"calls go through ctypes, some microseconds slower each ({e}); run "
+                      "__graft_entry__.build() with g++", RuntimeWarning, stacklevel=3)
+        return None
+    sys.modules[name] = module
+    return module
+
+
+_marshal = _load_marshal()
 
 
 def _check(rc: int) -> None:

@@ -1,7 +1,7 @@
 """Build of libzerostep.so (the gfx950 kernels and the C-ABI host layer), of
 libzerotwin.so (the benchmark's measurement aids, zero_twin.h), of
 workloads/libzerogen.so (the device side of the seeded input generators) and of
-_marshal.so (what the binding reads off tensors, host code).
+the binding's host library _marshal (what it reads off tensors).
 
 hipcc cross-compiles for gfx950 on any host, so this runs without a GPU.
 """
@@ -10,7 +10,13 @@ from __future__ import annotations
 import os
 import shutil
 import subprocess
+import sysconfig
 import tempfile
+import warnings
+from concurrent.futures import ThreadPoolExecutor
+from typing import Optional
+
+import torch
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -32,8 +38,10 @@ TWIN_SOURCES = [os.path.join(CSRC, "zero_twin.hip")]
 GEN_DIR = os.path.join(ROOT, "workloads", "csrc")
 GEN_LIB = os.path.join(ROOT, "workloads", "libzerogen.so")
 GEN_SOURCES = [os.path.join(GEN_DIR, "zero_gen.hip")]
-# host code against torch's and Python's headers, by g++
-MARSHAL_LIB = os.path.join(HERE, "_marshal.so")
+# host code against torch's and Python's headers, by g++: it holds internal symbols of
+# both, so each pair has a file of its own and none loads another's
+MARSHAL_LIB = os.path.join(HERE, f"_marshal.{sysconfig.get_config_var('SOABI')}."
+                                 f"torch-{torch.__version__}.so")
 MARSHAL_SOURCE = os.path.join(CSRC, "marshal.cpp")
 ARCH = "gfx950"
 
@@ -59,20 +67,50 @@ def hipcc() -> str:
     raise RuntimeError("hipcc not found (set HIPCC or install ROCm)")
 
 
-def marshal_command(out: str) -> list:
-    import sysconfig
+def _marshal_includes() -> list:
+    root = os.path.join(os.path.dirname(torch.__file__), "include")
+    return [root, os.path.join(root, "torch", "csrc", "api", "include"),
+            sysconfig.get_paths()["include"]]
 
-    import torch
-    root = os.path.dirname(torch.__file__)
-    gxx = shutil.which("g++")
-    if gxx is None:
-        raise RuntimeError("g++ not found")
-    return [gxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+
+def marshal_missing() -> Optional[str]:
+    """What its build lacks here, or None.  The package does without the library (train.py)."""
+    if shutil.which("g++") is None:
+        return "g++"
+    for header in ("torch/csrc/autograd/python_variable.h", "Python.h"):
+        if not any(os.path.exists(os.path.join(d, header)) for d in _marshal_includes()):
+            return header
+    return None
+
+
+def marshal_command(out: str) -> list:
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    return [shutil.which("g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-            "-isystem", os.path.join(root, "include"),
-            "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
-            "-isystem", sysconfig.get_paths()["include"], "-I", INCLUDE, MARSHAL_SOURCE, "-o", out,
-            "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10"]
+            *(a for d in _marshal_includes() for a in ("-isystem", d)), "-I", INCLUDE,
+            MARSHAL_SOURCE, "-o", out, "-L" + lib, "-ltorch_python", "-ltorch_cpu", "-ltorch",
+            "-lc10"]
+
+
+def build_marshal(verbose: bool = False) -> Optional[str]:
+    """Compile the binding's host library, written atomically.  Where that is not
+    possible a warning says why, and the binding goes without it."""
+    missing = marshal_missing()
+    if missing is None:
+        tmp = None
+        try:
+            tmp = _temp(MARSHAL_LIB)
+            _run_all([marshal_command(tmp)], verbose)
+            _put(tmp, MARSHAL_LIB)
+            return MARSHAL_LIB
+        except (RuntimeError, OSError) as e:
+            missing = str(e)
+        finally:
+            if tmp is not None and os.path.exists(tmp):
+                os.unlink(tmp)
+    warnings.warn(f"the binding's host library is not built, calls go through ctypes: {missing}",
+                  RuntimeWarning, stacklevel=2)
+    return None
 
 
 def code_text(src: str) -> str:
@@ -147,6 +185,19 @@ def _run_all(commands, verbose: bool) -> None:
                 proc.kill()
 
 
+def _temp(lib: str) -> str:
+    """A new file beside the library, to be put in its place."""
+    fd, tmp = tempfile.mkstemp(prefix=f".{os.path.basename(lib)}.", suffix=".tmp",
+                               dir=os.path.dirname(lib))
+    os.close(fd)
+    return tmp
+
+
+def _put(tmp: str, lib: str) -> None:
+    os.chmod(tmp, 0o755)  # g++ leaves the temporary file's mode, its owner's alone
+    os.replace(tmp, lib)
+
+
 def build(verbose: bool = False) -> str:
     """Compile the three libraries for gfx950, each source to an object (hipcc
     processes side by side), then each library from its objects, and the
@@ -155,15 +206,10 @@ def build(verbose: bool = False) -> str:
     compile_flags = [f for f in FLAGS if f != "-shared"]
     link_flags = [f"--offload-arch={ARCH}", "-fPIC", "-shared"]
     temps = []
-    with tempfile.TemporaryDirectory(prefix="zerostep_build_") as objdir:
+    with tempfile.TemporaryDirectory(prefix="zerostep_build_") as objdir, \
+            ThreadPoolExecutor(1) as beside:
+        host = beside.submit(build_marshal, verbose)
         try:
-            def temp(lib: str) -> str:
-                fd, tmp = tempfile.mkstemp(prefix=f".{os.path.basename(lib)}.", suffix=".tmp",
-                                           dir=os.path.dirname(lib))
-                os.close(fd)
-                temps.append(tmp)
-                return tmp
-
             compiles, links = [], []
             for lib, sources in libs:
                 objects = []
@@ -172,23 +218,24 @@ def build(verbose: bool = False) -> str:
                     objects.append(obj)
                     compiles.append([hipcc(), *compile_flags, "-I", INCLUDE, "-I", CSRC, "-I",
                                      GEN_DIR, "-o", obj, "-c", src])
-                tmp = temp(lib)
-                links.append((lib, tmp, [hipcc(), *link_flags, *objects, "-o", tmp]))
-            marshal = temp(MARSHAL_LIB)
-            _run_all([*compiles, marshal_command(marshal)], verbose)
+                temps.append(_temp(lib))
+                links.append((lib, temps[-1], [hipcc(), *link_flags, *objects, "-o", temps[-1]]))
+            _run_all(compiles, verbose)
             _run_all([cmd for _, _, cmd in links], verbose)
-            for lib, tmp in (*((lib, tmp) for lib, tmp, _ in links), (MARSHAL_LIB, marshal)):
-                os.chmod(tmp, 0o755)  # g++ leaves the temporary file's mode, its owner's alone
-                os.replace(tmp, lib)
+            for lib, tmp, _ in links:
+                _put(tmp, lib)
         finally:
             for tmp in temps:
                 if os.path.exists(tmp):
                     os.unlink(tmp)
+        host.result()
     return LIB
 
 
 def ensure_built() -> str:
-    """Build only if a library is missing."""
-    if not all(os.path.exists(p) for p in (LIB, TWIN_LIB, GEN_LIB, MARSHAL_LIB)):
+    """Build only what is missing."""
+    if not all(os.path.exists(p) for p in (LIB, TWIN_LIB, GEN_LIB)):
         build()
+    elif not os.path.exists(MARSHAL_LIB):
+        build_marshal()
     return LIB

@@ -61,8 +61,13 @@ def _declare() -> None:
 
 
 _declare()
-# the calls that a program makes often, without ctypes' conversions (csrc/marshal.cpp)
-_marshal.bind({name: ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in EXPORTED})
+# the calls that a program makes often, without ctypes' conversions (csrc/marshal.cpp) where
+# that library is there
+_calls = lib
+if _marshal is not None:
+    _marshal.bind({name: ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
+                   for name in EXPORTED})
+    _calls = _marshal
 
 
 def _optional_vec(t: Optional[torch.Tensor], n: int, kinds: dict, dev: torch.device, name: str):
@@ -100,7 +105,7 @@ def zero_embed(table: torch.Tensor, ids: torch.Tensor, y: torch.Tensor, *, scale
     tokens = ids.numel()
     pi, ib = _vec(ids, tokens, _INDEX, dev, "ids")
     py, dy, ldy = _like(y, (tokens, cols), _ELEM, dev, "y")
-    _run(_marshal.zero_embed, dev, pt, dt, vocab, cols, ldt, pi, ib, tokens, scale, py, dy, ldy,
+    _run(_calls.zero_embed, dev, pt, dt, vocab, cols, ldt, pi, ib, tokens, scale, py, dy, ldy,
          _raw_stream(stream, dev))
 
 
@@ -144,7 +149,7 @@ def zero_embed_backward(dy: torch.Tensor, ids: torch.Tensor, dtable: torch.Tenso
     if wide != cols:
         raise ValueError(f"dtable has rows of {wide}, dy of {cols}")
     pws, nws = _workspace(workspace, dev)
-    _run(_marshal.zero_embed_backward, dev, pd, dd, ldd, pi, ib, tokens, vocab, cols, scale, pt, dt,
+    _run(_calls.zero_embed_backward, dev, pd, dd, ldd, pi, ib, tokens, vocab, cols, scale, pt, dt,
          ldt, 1 if accumulate else 0, pws, nws, _raw_stream(stream, dev))
 
 
@@ -177,7 +182,7 @@ def zero_layernorm(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.T
     pq, ldq, ps, lds, fmt = _q8(q, s, rows, cols, dev, "q")
     pm = _optional_vec(mean, rows, _F32, dev, "mean")
     prstd = _optional_vec(rstd, rows, _F32, dev, "rstd")
-    _run(_marshal.zero_layernorm, dev, px, dx, ldx, pr, dr, ldr, pw, pb, dw, rows, cols, eps, ph,
+    _run(_calls.zero_layernorm, dev, px, dx, ldx, pr, dr, ldr, pw, pb, dw, rows, cols, eps, ph,
          ldh, py, dy, ldy, pq, fmt or ZERO_E4M3, ldq, ps, lds, pm, prstd, _raw_stream(stream, dev))
 
 
@@ -208,7 +213,7 @@ def zero_layernorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Ten
     if dw is not None and db is not None and ddw != ddb:
         raise TypeError(f"dw has dtype {dw.dtype}, db {db.dtype}")
     pws, nws = _workspace(workspace, dev)
-    _run(_marshal.zero_layernorm_backward, dev, pd, dd, ldd, ph, dh, ldh, pw, dwt, pm, prstd, pr,
+    _run(_calls.zero_layernorm_backward, dev, pd, dd, ldd, ph, dh, ldh, pw, dwt, pm, prstd, pr,
          dr, ldr, rows, cols, px, dxt, ldx, pdw, pdb,
          ddw if ddw is not None else ddb if ddb is not None else ZERO_F32, pws, nws,
          _raw_stream(stream, dev))
@@ -236,7 +241,7 @@ def zero_act(gate: torch.Tensor, kind: str, *, up: Optional[torch.Tensor] = None
     pq, ldq, ps, lds, fmt = _q8(q, s, rows, cols, dev, "q")
     pgq, ldgq, pgs, ldgs, ck = _q8(gate_q, gate_s, rows, cols, dev, "gate_q")
     puq, lduq, pus, ldus, ck = _q8(up_q, up_s, rows, cols, dev, "up_q", ck)
-    _run(_marshal.zero_act, dev, pg, ldg, pu, ldu, dt, code, rows, cols, py, dy, ldy, pq,
+    _run(_calls.zero_act, dev, pg, ldg, pu, ldu, dt, code, rows, cols, py, dy, ldy, pq,
          fmt or ZERO_E4M3, ldq, ps, lds, pgq, ck or ZERO_E4M3, ldgq, pgs, ldgs, puq, lduq, pus,
          ldus, _raw_stream(stream, dev))
 
@@ -260,7 +265,7 @@ def zero_act_backward(dy: torch.Tensor, gate_q: torch.Tensor, gate_s: torch.Tens
             raise TypeError(f"dup has dtype {dup.dtype}, dgate {dgate.dtype}")
         pu, _, ldu = _like(dup, shape, _ELEM, dev, "dup")
     py, dyt, ldy = (None, ZERO_F32, 0) if y is None else _like(y, shape, _ELEM, dev, "y")
-    _run(_marshal.zero_act_backward, dev, pd, dd, ldd, pgq, ck or ZERO_E4M3, ldgq, pgs, ldgs, puq,
+    _run(_calls.zero_act_backward, dev, pd, dd, ldd, pgq, ck or ZERO_E4M3, ldgq, pgs, ldgs, puq,
          lduq, pus, ldus, code, rows, cols, pg, ldg, pu, ldu, dx, py, dyt, ldy,
          _raw_stream(stream, dev))
 
@@ -294,7 +299,7 @@ def zero_logprob(logits: torch.Tensor, ids: Optional[torch.Tensor],
         ptl, _, ldl = _like(top_logit, (rows, top), _ELEM, dev, "top_logit")
         if ldl != ldt:
             raise ValueError("top_index and top_logit have different row strides")
-    _run(_marshal.zero_logprob, dev, p, dt, ld, rows, vocab, pi, ib, temperature, pl, pe, ps, pti,
+    _run(_calls.zero_logprob, dev, p, dt, ld, rows, vocab, pi, ib, temperature, pl, pe, ps, pti,
          ptl, top, ldt, _raw_stream(stream, dev))
 
 
@@ -319,5 +324,5 @@ def zero_logprob_backward(logits: torch.Tensor, ids: Optional[torch.Tensor], lse
     if grad.dtype != logits.dtype:
         raise TypeError(f"grad has dtype {grad.dtype}, logits {logits.dtype}")
     pg, _, ldg = _like(grad, shape, _ELEM, dev, "grad")
-    _run(_marshal.zero_logprob_backward, dev, p, dt, ld, rows, vocab, pi, ib, temperature, ps, pl,
+    _run(_calls.zero_logprob_backward, dev, p, dt, ld, rows, vocab, pi, ib, temperature, ps, pl,
          pe, pde, loss_scale, _distill_scale(dev, ctl), pg, ldg, _raw_stream(stream, dev))

@@ -75,7 +75,8 @@ _declare()
 
 # What a call looks at is written out below rather than wrapped in objects: a
 # short call's time is the host's.  The functions that read tensors are _marshal's
-# (csrc/marshal.cpp); these say what they do, and raise what there is to raise.
+# (csrc/marshal.cpp); these say what they do, raise what there is to raise, and take
+# their place where that library is not built for the running Python and torch.
 
 def _mat_checked(t: torch.Tensor, kinds: dict, dev: torch.device,
                  name: str) -> Tuple[int, int, int]:
@@ -144,8 +145,11 @@ def _q8_checked(data: Optional[torch.Tensor], scales: Optional[torch.Tensor], ro
     return p, ld, ps, lds, code
 
 
-_marshal.init(_mat_checked, _like_checked, _vec_checked, _q8_checked, _FP8, _SCALE)
-_mat, _like, _vec, _q8 = _marshal.mat, _marshal.like, _marshal.vec, _marshal.q8
+if _marshal is not None:
+    _marshal.init(_mat_checked, _like_checked, _vec_checked, _q8_checked, _FP8, _SCALE)
+    _mat, _like, _vec, _q8 = _marshal.mat, _marshal.like, _marshal.vec, _marshal.q8
+else:
+    _mat, _like, _vec, _q8 = _mat_checked, _like_checked, _vec_checked, _q8_checked
 
 
 def _device(t: torch.Tensor) -> torch.device:
