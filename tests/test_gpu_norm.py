@@ -355,3 +355,28 @@ def test_norm_in_place_where_rows_end_inside_a_pack(rows, cols, dtype):
         got = call(a["x"], a["res"], got_h, got_y)
         assert torch.equal(got_h, h) and torch.equal(got_y, y), (h_in, y_in)
         assert torch.equal(got[0], q) and torch.equal(got[1], s), (h_in, y_in)
+
+
+@pytest.mark.parametrize("dtype", [F16, F32])
+@pytest.mark.parametrize("rows,cols", [(700, 513), (900, 1025), (600, 1543), (500, 2561), (300, 8191),
+                                       (300, 9217), (280, 12289), (260, 16383)])
+def test_backward_in_place_where_the_last_pack_is_another_waves(rows, cols, dtype):
+    """The row's last eight elements belong to a wave whose neighbour writes some of
+    them: in place the bits of a call with arrays of its own, which is checked
+    against the definition.  (8191 and 16383: a lane beside, the same wave.)"""
+    dev = device()
+    print(f"case: norm backward in place {rows}x{cols} {dtype}", flush=True)
+    dy, h, dres = (_randn(k, rows, cols, dtype=dtype) for k in (1, 2, 3))
+    w, rstd = _randn(4, cols, dtype=F16), 1 + 0.1 * _randn(5, rows)
+    ws = torch.empty(zs.zero_rmsnorm_backward_workspace(rows, cols), dtype=torch.uint8, device=dev)
+    dx, dw, dw2 = torch.empty_like(dy), torch.empty_like(w), torch.empty_like(w)
+    zs.zero_rmsnorm_backward(dy, h, w, rstd, dx, dw, ws, dres=dres)
+    wx, ww = ref.rmsnorm_backward(dy, h, w, rstd, dres)
+    _assert_backward(dx, dw, wx, ww, dy, h, w, rstd, dres)
+    for turn in range(4):
+        for which in ("dres", "h", "dy"):
+            args = dict(dy=dy.clone(), h=h.clone(), dres=dres.clone())
+            out = args[which]
+            zs.zero_rmsnorm_backward(args["dy"], args["h"], w, rstd, out, dw2, ws,
+                                     dres=args["dres"])
+            assert torch.equal(out, dx) and torch.equal(dw, dw2), (which, turn)
