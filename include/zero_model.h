@@ -174,8 +174,13 @@ int zero_layernorm_backward(const void* dy, int32_t dy_dtype, int64_t ld_dy, con
  *   up_q, ld_uq, up_s, ld_us        up in the q8 layout (of ck_fmt), or NULL
  * The checkpoints are what zero_q8_quantize makes of gate and up, bit for bit;
  * y is of the elements themselves.  At least one output is given.  An infinite
- * gate gives the formula's limit where f's is infinite, else NaN.  Returns
- * ZERO_OK, ZERO_EINVAL, ZERO_EALIGN or ZERO_EHIP.
+ * gate gives the formula's limit where f's is infinite, else NaN.
+ *
+ * f comes from the hardware's exponential, whose argument is rounded.  For gates
+ * above 0 it is off by a few 2^-24 of its value; for gates below 0 also by up to
+ * 2^-24 |g| (SiLU), 2^-24 g^2 (GELU) or 5 * 2^-24 |2u| (its tanh form, u what the
+ * tanh is of).  SiLU is 0 below -87.3, where f is under 1.1e-36.  Returns ZERO_OK,
+ * ZERO_EINVAL, ZERO_EALIGN or ZERO_EHIP.
  */
 int zero_act(const void* gate, int64_t ld_g, const void* up, int64_t ld_u, int32_t x_dtype,
              int32_t kind, int64_t rows, int64_t cols, void* y, int32_t y_dtype, int64_t ld_y,
@@ -231,8 +236,9 @@ int zero_act_backward(const void* dy, int32_t dy_dtype, int64_t ld_dy, const voi
  *     alternative, which zero_distill turns into NaN.
  *   - An lse beyond fp32's range is infinite (logits / temperature of 3e38), logp and
  *     entropy are taken without it.  top_logit has no negative zeros.
- * The order of a row's sums follows from rows, vocab and dtype, so that the same row
- * among few and among many may differ in its last bits.
+ * The order of a row's sums follows from rows, vocab, dtype and the row's address
+ * modulo 16, so that the same row among few and among many, or at another place, may
+ * differ in its last bits.
  * Returns ZERO_OK, ZERO_EINVAL, ZERO_EALIGN, ZERO_ERANGE (top) or ZERO_EHIP.
  */
 int zero_logprob(const void* logits, int32_t dtype, int64_t ld, int64_t rows, int64_t vocab,

@@ -2,9 +2,11 @@
 //
 // Elementwise but for the largest magnitude of each block of 128, which is 16
 // neighbouring lanes' (eight elements a lane), and bound by HBM: a lane holds one
-// pack of each array.  8192 x 14336 fp16 gated, e4m3 output and checkpoints: 152 to 159
-// us, 5.2 to 5.4 TB/s; its gradient with y once more 203 us, 5.8 TB/s.  1003 x 5001 bf16,
-// GELU: 8.8 us for what 5.3 would carry, two rounds of waves and rows at odd addresses.
+// pack of each array.  8192 x 14336 fp16 gated, e4m3 output and checkpoints: 153 to 163
+// us, 5.1 to 5.4 TB/s, the vector units busy in three quarters of the cycles; its gradient
+// with y once more 198 to 203 us, 5.8 to 6.0 TB/s, half of them.  1003 x 5001 bf16, GELU:
+// 8.2 us for what a large copy's rate would carry in 4.1, a wave and a half for each place,
+// one trip to memory each.
 #include "zero_device.h"
 #include "zero_model_internal.h"
 
@@ -21,8 +23,11 @@ struct Slope {
     float s, d;
 };
 
-// 1 / (1 + exp(-v)) and 1 less that, both to a few units of fp32's last place at
-// either end: exp(-|v|) neither overflows nor cancels.
+// 1 / (1 + exp(-v)) and 1 less that: exp(-|v|) neither overflows nor cancels.  The larger
+// end is good to 3 half units of fp32's last place (2^-24).  The smaller has the error of
+// the exponent's product, which grows with |v|: SiLU's values are off by at most 10 half
+// units down to -9, 18 to -19, 32 to -33, 66 to -87; and it is 0 below -87.3, where fp32's
+// normal range ends.
 __device__ __forceinline__ Slope sigmoid(float v) {
     const float e = __builtin_amdgcn_exp2f(-fabsf(v) * kLog2e);
     const float big = __builtin_amdgcn_rcpf(1.0f + e), small = e * big;
@@ -33,18 +38,20 @@ __device__ __forceinline__ Slope sigmoid(float v) {
 template <int KIND, bool DERIVED>
 __device__ __forceinline__ Slope slope(float g) {
     if constexpr (KIND == ZERO_SILU && !DERIVED) {
-        // exp(-g) may overflow, and below -87, where f is under 1e-36, s is 0.  (By the
-        // form with both ends 8192 x 14336 162 us, 158 so.)
+        // exp(-g) may overflow; below -87.33, where f is under 1.03e-36, s is 0, as the
+        // other form's.  (By the form with both ends 8192 x 14336 162 us, 158 so.)
         return {__builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * g)), 0.0f};
     } else if constexpr (KIND == ZERO_SILU) {
         const Slope p = sigmoid(g);
         return {p.s, p.s * p.d};
     } else if constexpr (KIND == ZERO_GELU) {
         // With x = |g|: Phi(-x) = exp(-x^2 / 2) t P(t), t = 1 / (1 + x / 4), P a
-        // polynomial fitted to the scaled complementary error function (5e-8 of the
-        // value); Phi(x) = 1 - Phi(-x).  So small values of Phi keep their places, and
-        // the derivative's exponential serves both.  (With the library's complementary
-        // error function: 8192 x 2048 fp16 30 us, 19 with the tanh form.)
+        // polynomial fitted to the scaled complementary error function (itself to 5e-8 of
+        // the value); Phi(x) = 1 - Phi(-x).  So small values of Phi do not cancel, and the
+        // derivative's exponential serves both.  The exponent's products are rounded at
+        // x^2's size, which is most of the error: at most 9 half units (2^-24) of the value
+        // down to -2.2, 17 to -4.3, 55 to -8.7, 133 to -13; 6 above 0.  (With the library's
+        // complementary error function: 8192 x 2048 fp16 30 us, 21 so.)
         const float x = fabsf(g), t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.25f, x, 1.0f));
         const float e = __builtin_amdgcn_exp2f(-0.5f * kLog2e * x * x);
         float m = 0.019782092f;
@@ -61,7 +68,8 @@ __device__ __forceinline__ Slope slope(float g) {
         return {g < 0.0f ? tail : 1.0f - tail, 0.39894228f * e};
     } else {
         // (1 + tanh u) / 2 = 1 / (1 + exp(-2u)), u = k (g + 0.044715 g^3); both
-        // are 0 or 1 long before 64, and g^3 stays in range
+        // are 0 or 1 long before 64, and g^3 stays in range.  Off by 2u's roundings too, at
+        // most 25 half units down to -2.7, 57 to -4.7, 128 to -6.7, 202 to -8; 4 above 0
         constexpr float k2 = 1.5957691f, kCube = 0.044715f;
         const float x = g != g ? g : fminf(fmaxf(g, -64.0f), 64.0f), xx = x * x;
         const Slope p = sigmoid(k2 * x * __builtin_fmaf(kCube, xx, 1.0f));

@@ -90,8 +90,10 @@ K2, CUBE = math.sqrt(8 / math.pi), 0.044715
 def activation(kind, g):
     """f, f' and the bounds of their errors.  With v the argument of the sigmoid:
     exp2's argument is off by 2 u |v| and by what v is off, the instruction and
-    the reciprocal by a step each.  GELU: a rounding of erfc's argument turns into
-    2 g^2 of them, and erfc itself is off by at most 16 steps."""
+    the reciprocal by a step each.  GELU: of exp(-g^2 / 2) the three roundings of the
+    exponent are 1.5 g^2 u, the instruction a step; t = 1 / (1 + |g| / 4) is off by 3 u,
+    which t P(t) takes up to 3.2 times, the fit by u, the polynomial's and the other
+    products by less than 25 u."""
     g = g.double()
     if kind == "gelu":
         phi = torch.exp(-0.5 * g * g) / math.sqrt(2 * math.pi)
