@@ -1,10 +1,11 @@
 // Rows of a table by token, and the table's gradient.
 //
 // Forward: a gather, bound by the latency of id -> row -> store for few tokens (16 of
-// 131072 x 4096 fp16 2.3 us) and by HBM for many.
+// 131072 x 4096 fp16 2.3 us each in a graph) and by HBM for many (8192 tokens 19 us).
 //
 // Backward: the table's zeros are most of the bytes where the table is large (8192 tokens
-// of 131072 x 4096 fp16: 1.07 of 1.14 GB); 216 us then, of which they take 165 to 172.
+// of 131072 x 4096 fp16: 1.07 of 1.14 GB); 216 us then, of which they take 160 to 171.
+// Added to the table's rows instead, the same tokens take 54 us, in fp32 74.
 //
 // Backward of more than 512 tokens: they are sorted by their row of the table (a
 // stable radix sort of 9 bits a pass, so that equal ids keep the tokens' order), and
@@ -309,8 +310,9 @@ __device__ __forceinline__ void fill_zeros(const Fill& f, int64_t tile) {
 
 // All passes over up to kSmall tokens by one workgroup, the items in registers
 // during a pass and in LDS between passes, where the peers' bits are during one: 15 us
-// for 4096 tokens, 20 for 8192, 32 for 16384, mostly behind the zeros.  (By several
-// workgroups, two launches a pass, it takes 17 us, and nothing else goes on meanwhile.)
+// for 4096 tokens, 20 for 8192, 32 for 16384, behind the zeros where there are enough.
+// (By several workgroups, two launches a pass, it takes 13 to 17 us, and nothing else goes
+// on meanwhile.)
 constexpr int kPeersWords = kStartWaves * kBins * 2, kBinsWords = kStartWaves * kBins;
 __host__ __device__ inline int small_words(int rounds) {
     const int items = rounds * kStartLanes * 6 / 4;
@@ -863,9 +865,14 @@ hipError_t sort_many(SortPass p, uint32_t* const (&keys)[2], uint32_t* const (&o
     return hipGetLastError();
 }
 
-// Whether one workgroup sorts beside the zeros.  By several, in launches of their own, it
-// takes about 17 us whatever the number, so that beyond 8,192 tokens the zeros have to
-// hide what one takes more, 11 KB a token (16384 of 5000 x 64 fp16 45 us by one, 34 so).
+// Whether one workgroup sorts beside the zeros, or several in launches of their own.  Beyond
+// 8,192 tokens the zeros have to hide what one takes more, 11 KB a token (fp16, by one and
+// by several: 16384 of 5000 x 64 46 us and 30, of 32000 x 4096 108 and 120).  Up to that,
+// one: 8192 of 131072 x 4096 216 and 231, 4096 of 32000 x 512 31 and 37, 1024 of 1000 x 512
+// 21 and 24.  Where no zeros hide it, adding to the table, the two are alike up to 4,096
+// tokens (1024 of 1000 x 512 24 and 24, 4096 of 32000 x 512 30 and 30), but at 8,192 one
+// is the slower, which this rule does not tell apart (300 x 64 26 and 19, 131072 x 4096 54
+// and 48; with the few zeros of 300 x 64 25 and 20, of 1000 x 4096 46 and 42).
 bool one_sorts(int64_t tokens, int64_t zeros) {
     return tokens <= 8192 || (tokens <= kSmall && zeros / 11000 >= tokens - 8192);
 }

@@ -4,9 +4,9 @@
 // fp32, between the sum for the mean, the sum of squares about that mean (two
 // reductions, so that a row far from zero keeps its variance) and the outputs.
 //
-// 8192 x 4096 fp16 with an fp32 residual, h and an e4m3 output: 72 us, 5.1 TB/s, above
-// what a large copy reaches (4.75).  16 rows: 4.6 us, a launch, two trips to memory and
-// two reductions.
+// 8192 x 4096 fp16 with an fp32 residual, h and an e4m3 output: 72 us, 5.1 TB/s, of 6.2
+// that a large elementwise copy reaches.  16 rows: 4.5 us each in a graph, a launch, two
+// trips to memory and two reductions.
 #include "zero_device.h"
 #include "zero_model_internal.h"
 
@@ -170,11 +170,12 @@ hipError_t norm_shape(const LayerNormArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-// Up to 1,024 columns a row is a few lanes' of one wave, whose reductions need no barrier
-// (fp16, 262144 x 128 124 us with a workgroup per row, 44 so); wider ones a workgroup's.
-// Rows that end inside a pack load their last eight elements (8192 x 1023 24 us by
-// elements, 17 so; 8000 x 5001 93 and 78).  Above 16,384 columns a lane holds four or
-// eight packs: 1024 x 32768 56 us; with eight it spills, 1024 x 65536 207.
+// In fp16, with a residual and h: up to 1,024 columns a row is a few lanes' of one wave,
+// whose reductions need no barrier (262144 x 128 124 us with a workgroup per row, 43 so);
+// wider ones a workgroup's.  Rows that end inside a pack load their last eight elements
+// (8192 x 1023 24 us by elements, 17 so; 8000 x 5001 93 and 77).  Above 16,384 columns a
+// lane holds four or eight packs: 1024 x 32768 56 us; with eight it spills, 1024 x 65536
+// 206 (84 without a residual).
 hipError_t launch_layernorm(const LayerNormArgs& a, hipStream_t stream) {
     const int c = a.cols;
     if (c % 8 && c >= 8 && c <= 16384) {

@@ -2,8 +2,8 @@
 //
 // dx needs two sums over its row, mean(g) and mean(g xhat); dw and db are sums over
 // rows.  Bound by HBM: one pass over the arrays for rows of 8 to 16,384 columns.
-// 16387 x 1001 bf16 with dresidual: 26 us for dx and the partial rows (5.1 TB/s), 4.6 for
-// dw and db from them; 8192 x 4096 fp16 55 us.
+// 16387 x 1001 bf16 with dresidual: 26 us for dx and the partial rows (5.1 TB/s), 4.7 for
+// dw and db from them; 8192 x 4096 fp16 56 us, 59 to 63 with dresidual.
 #include "zero_device.h"
 #include "zero_model_internal.h"
 
@@ -301,8 +301,8 @@ __global__ __launch_bounds__(kDwThreads) void layernorm_dw_kernel(const float* p
 }
 
 // How a row's width is dealt with: lanes of a wave per row, or 0 for the workgroup,
-// or -1 for rows read twice.  (16387 x 1001 bf16: 150 us read twice, 31 by a wave; 1024 x
-// 32768 fp16, read twice, 130 us, 1.5 TB/s.)
+// or -1 for rows read twice.  (16387 x 1001 bf16: 150 us read twice, 30 by a wave; 1024 x
+// 32768 fp16, read twice, 100 us, 2.0 TB/s, 127 with dresidual.)
 int lanes_per_row(int cols) {
     if (cols < 8 || cols > 16384) return -1;
     return cols <= 128 ? 16 : cols <= 256 ? 32 : cols <= 1024 ? 64 : 0;

@@ -13,9 +13,10 @@
 // lie on the border, as in long ties, the row is read again for the exact value of the
 // top-th largest, and its ties are taken in the order of their places.
 //
-// Bound by HBM with many rows: 4096 x 131072 fp16 196 us, 222 with 64 alternatives (5.5
-// and 4.8 TB/s); and by the row's chain (load, sums, borders, places) with few: 37 x
-// 32001 bf16 with 20 alternatives 10 us.
+// Bound by HBM with many rows: 4096 x 131072 fp16 190 us, 204 to 218 with 64 alternatives
+// (5.7 and 4.9 to 5.3 TB/s), the vector units busy in three quarters of the cycles; and by
+// the row's chain (load, sums, borders, places) with few: 37 x 32001 bf16 with 20
+// alternatives 10 us.
 #include "zero_device.h"
 #include "zero_model_internal.h"
 
@@ -28,7 +29,8 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
 constexpr float kLowest = -3.402823466e38f;
 constexpr float kFar = -200.0f;  // 2^-200 is 0 in fp32
 
-// 2^x by the hardware's instruction: one step off at most
+// 2^x by the hardware's instruction: one step off at most, for x as it is rounded, which
+// is off by 2^-24 |x| itself
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
 struct Stat {
@@ -530,8 +532,8 @@ __device__ __forceinline__ bool put_row(const LogprobArgs& a, int64_t row_at, in
 // ---- a wave per row ----------------------------------------------------------
 // Rows of up to 2,048 stay in a wave's registers, four packs a lane, and need no
 // barrier.  The top-th largest of the 256 packs' maxima is the border; the logits
-// that reach it take their places in LDS by ballots.  65536 x 256 fp16 31 us, 75 with 20
-// alternatives (a workgroup per row 196 and 275).
+// that reach it take their places in LDS by ballots.  65536 x 256 fp16 31 us, 74 with 20
+// alternatives (a workgroup per row 196 and 275); 65536 x 2000 56 and 119.
 
 constexpr int kWavePacks = 4, kWaveRows = 4;
 constexpr int kWaveEntries = 256;
@@ -752,7 +754,11 @@ hipError_t logprob_size(const LogprobArgs& a, hipStream_t stream) {
     // Many rows go by in small workgroups, so that others load while one settles its
     // alternatives; few rows have a CU each to themselves.  fp16, with 64 alternatives,
     // by 256, 512 and 1,024 lanes: 4096 x 131072 226, 233 and 266 us, 8192 x 20000 116,
-    // 135 and 207, 1024 x 131072 73, 68 and 77, 256 x 131072 46, 36 and 33.
+    // 135 and 207, 1024 x 131072 73, 68 and 77, 256 x 131072 46, 36 and 33.  Up to 16,384
+    // logits the row could be held by 512 lanes; gone by and held, with 20 alternatives:
+    // 8192 x 12000 73 and 88 us, 2048 x 12000 24 and 27.  (With 512 to 2,047 rows held is
+    // the faster, which this rule does not tell apart: 1024 x 16384 20 and 16, 512 x 12000
+    // 12.1 and 11.1; without alternatives they are alike.)
     if (a.rows >= 2048) return run(logprob_kernel<DT, 256, 4, true, TOP>, 256);
     if (a.rows >= 512) return run(logprob_kernel<DT, 512, 4, true, TOP>, 512);
     if (a.vocab <= 512 * 4 * 8) return run(logprob_kernel<DT, 512, 4, false, TOP>, 512);

@@ -7,9 +7,9 @@
 // is written as loaded, read down its columns, and the 8-bit result is turned
 // once more so that stores run along qt's rows.
 //
-// Bound by HBM: 14336 x 4096 fp16 in both forms takes 50 us, 4.7 TB/s, as a large
-// copy (69 us with scaling and conversion as instructions of their own); by
-// rows alone 36, transposed alone 38.
+// Bound by HBM: 14336 x 4096 fp16 in both forms takes 50 us, 4.7 TB/s, of 6.2 that a
+// large elementwise copy reaches (69 us with scaling and conversion as instructions of
+// their own); by rows alone 36, transposed alone 38.
 #include "zero_device.h"
 #include "zero_train_internal.h"
 
