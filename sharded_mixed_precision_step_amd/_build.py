@@ -92,6 +92,15 @@ def marshal_command(out: str) -> list:
             "-lc10"]
 
 
+def _drop_marshals() -> None:
+    """Remove host libraries of earlier builds, of every Python and torch: they may call
+    the others by signatures that those no longer have."""
+    folder = os.path.dirname(MARSHAL_LIB)
+    for name in os.listdir(folder):
+        if name.startswith("_marshal.") and name.endswith(".so"):
+            os.unlink(os.path.join(folder, name))
+
+
 def build_marshal(verbose: bool = False) -> Optional[str]:
     """Compile the binding's host library, written atomically.  Where that is not
     possible a warning says why, and the binding goes without it."""
@@ -208,6 +217,7 @@ def build(verbose: bool = False) -> str:
     temps = []
     with tempfile.TemporaryDirectory(prefix="zerostep_build_") as objdir, \
             ThreadPoolExecutor(1) as beside:
+        _drop_marshals()
         host = beside.submit(build_marshal, verbose)
         try:
             compiles, links = [], []
